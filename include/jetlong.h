@@ -71,6 +71,8 @@ typedef enum {
                                      into the workspace (size it with this
                                      flag) and the grouped visits load them;
                                      same result, more HBM traffic           */
+#define JL_FLAG_ROTATE 0x8u       /* jl_paged_append: k (and q) arrive before
+                                     RoPE and are rotated by the call        */
 
 /* Human-readable name of a status code (static string). */
 const char *jl_status_string(jl_status s);
@@ -294,6 +296,151 @@ jl_status jl_bifocal_decode_noalloc(const void *q, const void *k_cache,
  * no error.  NULL error_word: JL_ERR_INVALID_ARG; a failed copy: JL_ERR_CUDA.
  */
 jl_status jl_bifocal_decode_noalloc_error(int32_t *error_word, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged cache.  (Additions of this library; the paper's decode reads one
+ * contiguous cache.)
+ *
+ *   k_pages, v_pages  [n_pages, P, Hkv, D]: pools of pages of P tokens, P a
+ *                power of two from 16 to 256.  The last three dimensions are
+ *                contiguous; page_stride is the distance between pages in
+ *                elements, the same for both pools (at least P Hkv D, a
+ *                multiple of 16 bytes), so K and V may be interleaved.
+ *   page_summary [n_pages, Hkv, 2, D] in the cache's dtype, contiguous: the
+ *                least ([.., 0, :]) and greatest ([.., 1, :]) value of each
+ *                channel over the page's keys.  NaN keys give NaN.
+ *   block_table  [batch, max_pages] device int32, rows table_stride elements
+ *                apart: pool page of logical page c of sequence b, which
+ *                holds keys cP .. cP + P - 1.  An entry outside
+ *                [0, n_pages) is a page that is not there.  Sequences may
+ *                share pages that nobody writes.
+ *   seqlens      [batch] device int32, L_b with the new tokens included.
+ * max_pages * P <= 2^30.  Head counts: n_q_heads a multiple of n_kv_heads,
+ * any group size; head_dim 64 or 128; batch <= 65535; JL_BF16 or JL_FP32.
+ * All tables and lengths live on the device and are read when the kernels
+ * run, so a captured call replays with the values of the moment.
+ */
+
+/*
+ * jl_paged_append - rotate new tokens and write them into their pages.
+ *
+ * Sequence b's new tokens are rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 of k,
+ * v and q; the last of them is at position L_b - 1.
+ *   k, v         [total_tokens, Hkv, D]
+ *   page_summary updated for every page written (NULL: none is kept): from
+ *                the new keys alone where the page's first token is among
+ *                them, else together with what it held
+ *   q, q_out     [total_tokens, Hq, D], rotated like k (q_out may be q); both
+ *                NULL if not wanted.  Only with JL_FLAG_ROTATE.
+ *   cu_seqlens   [batch + 1] device int32 prefix sums
+ *   max_new      >= every sequence's number of new tokens (sizes the grid)
+ *   rope_theta   used with JL_FLAG_ROTATE: pair k turns by
+ *                p theta^(-2k/D) at position p (angles in 64 bits, the
+ *                products in fp32, rounded once).  Without the flag k is
+ *                stored as given.
+ * A sequence with no new tokens is left alone, and so is one whose numbers do
+ * not fit (more new tokens than L_b or max_new, rows past total_tokens).
+ * Tokens of a page that is not there are not written (their q_out is).  The
+ * pages written by one call must be distinct.
+ */
+jl_status jl_paged_append(const void *k, const void *v, void *k_pages,
+                          void *v_pages, void *page_summary,
+                          const int32_t *block_table, int64_t table_stride,
+                          int32_t max_pages, const int32_t *cu_seqlens,
+                          const int32_t *seqlens, int32_t batch,
+                          int32_t total_tokens, int32_t max_new,
+                          int32_t n_q_heads, int32_t n_kv_heads,
+                          int32_t head_dim, int32_t page_size,
+                          int32_t n_pages, int64_t page_stride, const void *q,
+                          void *q_out, double rope_theta, jl_dtype dtype,
+                          uint32_t flags, void *stream);
+
+/*
+ * jl_bifocal_select_pages - the pages that each sequence's new token should
+ * read, for jl_bifocal_decode_paged.
+ *
+ * With i = L_b - 1, G = G(L_b), n(p) = p - floor(p / G), and m = cP + P/2 the
+ * middle key of logical page c, the query is turned as the bifocal rule turns
+ * it against that key, q' = R(n(m) - n(i)) q (q' = q for i - m < w0), and
+ *     score(c) = max over the kv head's query heads of
+ *                sum_d max(q'_d min_d, q'_d max_d).
+ * That bounds from above the unscaled score of every key whose shift is the
+ * middle key's (all of the page's when G = 1).  A score that is not finite
+ * ranks first.  A page that is not there ranks last.
+ *   q          [B, Hq, D]   standard RoPE at position L_b - 1
+ *   page_list  [B, Hkv, n_select] int32 out, ascending logical pages: the
+ *              n_first first pages, the n_last newest ones and the highest
+ *              scores among the others, n_select in all; every page of a
+ *              sequence that has no more than n_select.  -1 behind the last.
+ *              Scores are compared as if formed in 64 bits; the lower page
+ *              wins a tie.
+ *   n_select >= 1;  n_first, n_last >= 0, n_first + n_last <= n_select
+ *   workspace  >= jl_bifocal_select_pages_workspace_size(...) bytes, 256-byte
+ *              aligned, no initialisation needed
+ * L_b = 0, or a length past max_pages P, lists nothing.
+ */
+size_t jl_bifocal_select_pages_workspace_size(int32_t batch,
+                                              int32_t n_kv_heads,
+                                              int32_t max_pages,
+                                              int32_t n_select);
+
+jl_status jl_bifocal_select_pages(const void *q, const void *page_summary,
+                                  const int32_t *block_table,
+                                  int64_t table_stride, int32_t max_pages,
+                                  const int32_t *seqlens, int32_t batch,
+                                  int32_t n_q_heads, int32_t n_kv_heads,
+                                  int32_t head_dim, int32_t page_size,
+                                  int32_t n_pages, int32_t n_select,
+                                  int32_t n_first, int32_t n_last,
+                                  int64_t w_pretrained, int32_t w0,
+                                  double rope_theta, int32_t *page_list,
+                                  void *workspace, size_t workspace_bytes,
+                                  jl_dtype dtype, uint32_t flags,
+                                  void *stream);
+
+/*
+ * jl_bifocal_decode_paged - jl_bifocal_decode over a paged cache: one new
+ * token per sequence, split over the cache's length and joined.
+ *
+ *   q          [B, Hq, D]   standard RoPE at position L_b - 1
+ *   page_list  [B, Hkv, n_list] device int32, or NULL: attend only to the
+ *              keys of the listed logical pages.  Entries outside
+ *              [0, max_pages) and pages past the length are skipped; an entry
+ *              given twice counts twice.
+ *   n_list     <= 2^20; 0 with a NULL page_list
+ *   window     0, or W >= 1: only keys max(0, L_b - W) .. L_b - 1
+ *   out        [B, Hq, D];  lse [B, Hq] fp32 or NULL
+ *   workspace  >= jl_bifocal_decode_paged_workspace_size(...) bytes, 256-byte
+ *              aligned, no initialisation needed; its first int32 is the
+ *              kernels' error word, 0 after a good call (as for
+ *              jl_bifocal_decode).  Calls that overlap on the GPU need one
+ *              each.
+ * A sequence with no visible key (L_b = 0, a length past max_pages P, no page
+ * of the list there) gets zeros and LSE = -inf.  Keys of pages that are not
+ * there are not visible.  Scores, softmax statistics and outputs are held in
+ * fp32; in bf16, keys that the bifocal rule turns and the softmax weights are
+ * carried as pairs of bf16, so neither is rounded to eight bits.  The work is
+ * divided over the SMs on the device, from the lengths, in a fixed order:
+ * equal inputs give equal bits.
+ */
+size_t jl_bifocal_decode_paged_workspace_size(int32_t batch, int32_t head_dim);
+
+jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages,
+                                  const void *v_pages,
+                                  const int32_t *block_table,
+                                  int64_t table_stride, int32_t max_pages,
+                                  const int32_t *seqlens,
+                                  const int32_t *page_list, int32_t n_list,
+                                  int32_t batch, int32_t n_q_heads,
+                                  int32_t n_kv_heads, int32_t head_dim,
+                                  int32_t page_size, int32_t n_pages,
+                                  int64_t page_stride, int64_t w_pretrained,
+                                  int32_t w0, int32_t window,
+                                  double rope_theta, void *out, float *lse,
+                                  void *workspace, size_t workspace_bytes,
+                                  jl_dtype dtype, uint32_t flags,
+                                  void *stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

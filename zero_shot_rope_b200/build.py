@@ -12,7 +12,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libjetlong.so")
-SOURCES = ["jl_api.cu", "jl_simt.cu", "jl_decode.cu", "jl_decode_sm100.cu", "jl_prefill_sm100.cu"]
+SOURCES = ["jl_api.cu", "jl_simt.cu", "jl_decode.cu", "jl_decode_sm100.cu", "jl_prefill_sm100.cu",
+           "jl_paged_append.cu", "jl_paged_select.cu", "jl_paged_decode.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -7,6 +7,7 @@
 
 #include "../../include/jetlong.h"
 #include "jl_common.cuh"
+#include "jl_paged.cuh"
 
 namespace jl {
 cudaError_t launch_simt_prefill(bool bf16, int D, const void *q, const void *k, const void *v, void *out,
@@ -81,6 +82,40 @@ jl_status check_method(int64_t w_pre, int32_t w0, double theta) {
 
 jl_status cuda_fail(cudaError_t e, const char *what) {
   return fail(JL_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// What the paged-cache calls check alike.
+jl_status check_pages(int32_t page_size, int32_t n_pages, int32_t max_pages, int64_t table_stride, int32_t batch,
+                      jl_dtype dtype) {
+  if (dtype != JL_BF16 && dtype != JL_FP32) return fail(JL_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  if (page_size < 1 || (page_size & (page_size - 1)) != 0)
+    return fail(JL_ERR_INVALID_ARG, "page_size must be a power of two (got %d)", page_size);
+  if (page_size < (1 << jl::PG_MIN_LOG2) || page_size > (1 << jl::PG_MAX_LOG2))
+    return fail(JL_ERR_UNSUPPORTED, "page_size %d not supported (%d to %d)", page_size, 1 << jl::PG_MIN_LOG2,
+                1 << jl::PG_MAX_LOG2);
+  if (n_pages < 1 || max_pages < 1)
+    return fail(JL_ERR_INVALID_ARG, "n_pages and max_pages must be >= 1 (got %d, %d)", n_pages, max_pages);
+  if ((int64_t)max_pages * page_size > (int64_t)1 << 30)
+    return fail(JL_ERR_UNSUPPORTED, "max_pages * page_size (%lld) exceeds 2^30", (long long)max_pages * page_size);
+  if (table_stride < max_pages)
+    return fail(JL_ERR_INVALID_ARG, "table_stride (%lld) < max_pages (%d)", (long long)table_stride, max_pages);
+  if (batch < 0) return fail(JL_ERR_INVALID_ARG, "batch must be >= 0");
+  if (batch > 65535) return fail(JL_ERR_UNSUPPORTED, "batch %d exceeds 65535 sequences per call", batch);
+  return JL_OK;
+}
+
+jl_status check_pool(int32_t page_size, int64_t page_stride, int32_t Hkv, int32_t D, jl_dtype dtype) {
+  if (page_stride < (int64_t)page_size * Hkv * D)
+    return fail(JL_ERR_INVALID_ARG, "page_stride (%lld) < page_size * n_kv_heads * head_dim", (long long)page_stride);
+  if (page_stride % (dtype == JL_BF16 ? 8 : 4) != 0)
+    return fail(JL_ERR_INVALID_ARG, "page_stride (%lld elements) is not a multiple of 16 bytes", (long long)page_stride);
+  return JL_OK;
+}
+
+int log2_of(int32_t x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
 }
 
 }  // namespace
@@ -266,6 +301,189 @@ jl_status jl_bifocal_decode(const void *q, const void *k_cache, const void *v_ca
   return jl_bifocal_decode_window(q, k_cache, v_cache, seqlens, batch, cache_capacity, max_seqlen, n_q_heads,
                                   n_kv_heads, head_dim, w_pretrained, w0, 0, rope_theta, out, lse, workspace,
                                   workspace_bytes, dtype, flags, stream);
+}
+
+// ------------------------------------------------------------- paged cache
+jl_status jl_paged_append(const void *k, const void *v, void *k_pages, void *v_pages, void *page_summary,
+                          const int32_t *block_table, int64_t table_stride, int32_t max_pages,
+                          const int32_t *cu_seqlens, const int32_t *seqlens, int32_t batch, int32_t total_tokens,
+                          int32_t max_new, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                          int32_t page_size, int32_t n_pages, int64_t page_stride, const void *q, void *q_out,
+                          double rope_theta, jl_dtype dtype, uint32_t flags, void *stream) {
+  jl_status s;
+  if ((s = check_heads(n_q_heads, n_kv_heads, head_dim)) != JL_OK) return s;
+  if (n_kv_heads > kMaxGridY)
+    return fail(JL_ERR_UNSUPPORTED, "n_kv_heads %d exceeds %d per call", n_kv_heads, kMaxGridY);
+  if ((s = check_pages(page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
+  if ((s = check_pool(page_size, page_stride, n_kv_heads, head_dim, dtype)) != JL_OK) return s;
+  if (flags & ~(uint32_t)JL_FLAG_ROTATE) return fail(JL_ERR_INVALID_ARG, "unknown or unfitting flag bits 0x%x", flags);
+  const bool rotate = (flags & JL_FLAG_ROTATE) != 0;
+  if (rotate && (s = check_method(1, 0, rope_theta)) != JL_OK) return s;
+  if ((q == nullptr) != (q_out == nullptr)) return fail(JL_ERR_INVALID_ARG, "q and q_out go together");
+  if (q != nullptr && !rotate) return fail(JL_ERR_INVALID_ARG, "q needs JL_FLAG_ROTATE");
+  if (total_tokens < 0 || max_new < 0) return fail(JL_ERR_INVALID_ARG, "total_tokens and max_new must be >= 0");
+  if (batch == 0 || total_tokens == 0) return ok();
+  if (max_new == 0 || max_new > total_tokens)
+    return fail(JL_ERR_INVALID_ARG, "max_new must be in [1, total_tokens] (got %d)", max_new);
+  if (k == nullptr || v == nullptr || k_pages == nullptr || v_pages == nullptr || block_table == nullptr ||
+      cu_seqlens == nullptr || seqlens == nullptr)
+    return fail(JL_ERR_INVALID_ARG, "k, v, k_pages, v_pages, block_table, cu_seqlens and seqlens must be non-NULL");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(page_summary) ||
+      !aligned16(q) || !aligned16(q_out))
+    return fail(JL_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  jl::PagedAppendArgs a;
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.summary = page_summary;
+  a.q_out = q_out;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.cu = cu_seqlens;
+  a.seqlens = seqlens;
+  a.max_pages = max_pages;
+  a.page_log2 = log2_of(page_size);
+  a.n_pages = n_pages;
+  a.T = total_tokens;
+  a.max_new = max_new;
+  a.Hkv = n_kv_heads;
+  a.GS = n_q_heads / n_kv_heads;
+  a.page_stride = page_stride;
+  const jl::InvFreq inv = make_inv_freq(head_dim, rotate ? rope_theta : 1.0);
+  const cudaError_t e = jl::launch_paged_append(dtype == JL_BF16, head_dim, rotate, a, inv, batch, (cudaStream_t)stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "paged append launch");
+}
+
+size_t jl_bifocal_select_pages_workspace_size(int32_t batch, int32_t n_kv_heads, int32_t max_pages, int32_t n_select) {
+  if (batch <= 0 || n_kv_heads <= 0 || max_pages <= 0 || n_select <= 0 || max_pages <= n_select) return 0;
+  const size_t n = (size_t)batch * n_kv_heads * max_pages;
+  return 3 * align256(n * sizeof(float)) + align256(n * sizeof(double));
+}
+
+jl_status jl_bifocal_select_pages(const void *q, const void *page_summary, const int32_t *block_table,
+                                  int64_t table_stride, int32_t max_pages, const int32_t *seqlens, int32_t batch,
+                                  int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t page_size,
+                                  int32_t n_pages, int32_t n_select, int32_t n_first, int32_t n_last,
+                                  int64_t w_pretrained, int32_t w0, double rope_theta, int32_t *page_list,
+                                  void *workspace, size_t workspace_bytes, jl_dtype dtype, uint32_t flags,
+                                  void *stream) {
+  jl_status s;
+  if ((s = check_heads(n_q_heads, n_kv_heads, head_dim)) != JL_OK) return s;
+  if ((s = check_method(w_pretrained, w0, rope_theta)) != JL_OK) return s;
+  if ((s = check_pages(page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
+  if (flags & ~(uint32_t)JL_FLAG_PLAIN_CAUSAL) return fail(JL_ERR_INVALID_ARG, "unknown or unfitting flag bits 0x%x", flags);
+  if (n_select < 1) return fail(JL_ERR_INVALID_ARG, "n_select must be >= 1 (got %d)", n_select);
+  if (n_first < 0 || n_last < 0 || (int64_t)n_first + n_last > n_select)
+    return fail(JL_ERR_INVALID_ARG, "need n_first, n_last >= 0 and n_first + n_last <= n_select (got %d, %d, %d)", n_first,
+                n_last, n_select);
+  if (batch == 0) return ok();
+  if (q == nullptr || page_summary == nullptr || block_table == nullptr || seqlens == nullptr || page_list == nullptr)
+    return fail(JL_ERR_INVALID_ARG, "q, page_summary, block_table, seqlens and page_list must be non-NULL");
+  if (!aligned16(q) || !aligned16(page_summary)) return fail(JL_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  const size_t need = jl_bifocal_select_pages_workspace_size(batch, n_kv_heads, max_pages, n_select);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return fail(JL_ERR_WORKSPACE, "page selection needs %zu workspace bytes (got %zu)", need, workspace_bytes);
+  if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(JL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const size_t n = (size_t)batch * n_kv_heads * max_pages;
+  jl::PagedSelectArgs a;
+  a.q = q;
+  a.summary = page_summary;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.seqlens = seqlens;
+  a.B = batch;
+  a.Hkv = n_kv_heads;
+  a.GS = n_q_heads / n_kv_heads;
+  a.max_pages = max_pages;
+  a.page_log2 = log2_of(page_size);
+  a.n_pages = n_pages;
+  a.n_select = n_select;
+  a.n_first = n_first;
+  a.n_last = n_last;
+  a.w_pre = w_pretrained;
+  a.w0 = w0;
+  a.plain = (flags & JL_FLAG_PLAIN_CAUSAL) ? 1 : 0;
+  a.list = page_list;
+  a.score = (float *)workspace;
+  a.mx = (float *)((char *)workspace + align256(n * sizeof(float)));
+  a.amb = (int32_t *)((char *)workspace + 2 * align256(n * sizeof(float)));
+  a.fine = (double *)((char *)workspace + 3 * align256(n * sizeof(float)));
+  const jl::InvFreq inv = make_inv_freq(head_dim, rope_theta);
+  const cudaError_t e = jl::launch_paged_select(dtype == JL_BF16, head_dim, a, inv, (cudaStream_t)stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "page selection launch");
+}
+
+size_t jl_bifocal_decode_paged_workspace_size(int32_t batch, int32_t head_dim) {
+  if (batch <= 0 || head_dim <= 0) return 0;
+  const size_t rows = (size_t)2 * jl::PD_MAX_CTAS * jl::PD_HEADS;
+  return 256 + align256(rows * head_dim * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
+         align256(((size_t)batch + 1) * sizeof(long long));
+}
+
+jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                                  int64_t table_stride, int32_t max_pages, const int32_t *seqlens,
+                                  const int32_t *page_list, int32_t n_list, int32_t batch, int32_t n_q_heads,
+                                  int32_t n_kv_heads, int32_t head_dim, int32_t page_size, int32_t n_pages,
+                                  int64_t page_stride, int64_t w_pretrained, int32_t w0, int32_t window,
+                                  double rope_theta, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                  jl_dtype dtype, uint32_t flags, void *stream) {
+  jl_status s;
+  if (window < 0) return fail(JL_ERR_INVALID_ARG, "window must be >= 0 (0: no window), got %d", window);
+  if ((s = check_heads(n_q_heads, n_kv_heads, head_dim)) != JL_OK) return s;
+  if (n_q_heads > kMaxGridY)
+    return fail(JL_ERR_UNSUPPORTED, "n_q_heads %d exceeds %d per call", n_q_heads, kMaxGridY);
+  if ((s = check_method(w_pretrained, w0, rope_theta)) != JL_OK) return s;
+  if ((s = check_pages(page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
+  if ((s = check_pool(page_size, page_stride, n_kv_heads, head_dim, dtype)) != JL_OK) return s;
+  if (flags & ~(uint32_t)JL_FLAG_PLAIN_CAUSAL) return fail(JL_ERR_INVALID_ARG, "unknown or unfitting flag bits 0x%x", flags);
+  if (n_list < 0 || n_list > (1 << 20)) return fail(JL_ERR_INVALID_ARG, "n_list must be in [0, 2^20] (got %d)", n_list);
+  if (page_list == nullptr && n_list != 0) return fail(JL_ERR_INVALID_ARG, "n_list without a page_list");
+  if (batch == 0) return ok();
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || block_table == nullptr || seqlens == nullptr ||
+      out == nullptr)
+    return fail(JL_ERR_INVALID_ARG, "q, k_pages, v_pages, block_table, seqlens and out must be non-NULL");
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
+    return fail(JL_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  const size_t need = jl_bifocal_decode_paged_workspace_size(batch, head_dim);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(JL_ERR_WORKSPACE, "paged decode needs %zu workspace bytes (got %zu)", need, workspace_bytes);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(JL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const size_t rows = (size_t)2 * jl::PD_MAX_CTAS * jl::PD_HEADS;
+  jl::PagedDecodeArgs a;
+  a.q = q;
+  a.k = k_pages;
+  a.v = v_pages;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.seqlens = seqlens;
+  a.list = page_list;
+  a.n_list = n_list;
+  a.max_pages = max_pages;
+  a.page_log2 = log2_of(page_size);
+  a.n_pages = n_pages;
+  a.page_stride = page_stride;
+  a.B = batch;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.GS = n_q_heads / n_kv_heads;
+  a.HB = (a.GS + jl::PD_HEADS - 1) / jl::PD_HEADS;
+  a.w_pre = w_pretrained;
+  a.w0 = w0;
+  a.window = window;
+  a.plain = (flags & JL_FLAG_PLAIN_CAUSAL) ? 1 : 0;
+  a.err = (int *)workspace;
+  a.part_o = (float *)((char *)workspace + 256);
+  a.part_ml = (float *)((char *)a.part_o + align256(rows * head_dim * sizeof(float)));
+  a.tab = (long long *)((char *)a.part_ml + align256(rows * 2 * sizeof(float)));
+  a.out = out;
+  a.lse = lse;
+  const jl::InvFreq inv = make_inv_freq(head_dim, rope_theta);
+  const cudaError_t e = jl::launch_paged_decode(dtype == JL_BF16, head_dim, a, inv, (cudaStream_t)stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "paged decode launch");
 }
 
 }  // extern "C"

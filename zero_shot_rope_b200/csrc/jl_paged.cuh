@@ -1,0 +1,199 @@
+// Shared declarations of the paged-cache operators: append, page selection
+// and decode.
+//
+// The cache is a pool of pages [n_pages, P, Hkv, D] (K and V each; the first
+// stride is the caller's), P a power of two from 16 to 256.  Logical page c
+// of sequence b, its keys cP .. cP + P - 1, is pool page table[b, c].
+#pragma once
+
+#include "jl_common.cuh"
+
+namespace jl {
+
+// Minimum / maximum that keep a NaN: a NaN key must show in its page's range and
+// in the output, not vanish from a comparison.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr int PG_MIN_LOG2 = 4, PG_MAX_LOG2 = 8;  // page sizes 16 .. 256
+
+// ------------------------------------------------------------------ decode
+// Keys are processed in tiles of 64 consecutive cache slots, each made of four
+// 16-key blocks; a block lies inside one page (P >= 16).
+constexpr int PD_TILE = 64;
+constexpr int PD_BLK = 16;
+constexpr int PD_HEADS = 8;     // query heads a CTA serves at a time (of one kv head)
+constexpr int PD_MAX_CTAS = 296;
+
+struct PagedDecodeArgs {
+  const void *q, *k, *v;          // k, v: the pools
+  const int32_t *table;           // [B, max_pages], row stride table_stride
+  long long table_stride;
+  const int32_t *seqlens;
+  const int32_t *list;            // [B, Hkv, n_list] logical pages, or NULL: every page
+  int n_list, max_pages, page_log2, n_pages;
+  long long page_stride;          // elements between pages of a pool
+  int B, Hq, Hkv, GS, HB;         // HB: blocks of PD_HEADS query heads per kv head
+  long long w_pre;
+  int w0, window, plain;
+  float *part_o;                  // [2 * CTAs][PD_HEADS][D]
+  float *part_ml;                 // [2 * CTAs][PD_HEADS][2]
+  long long *tab;                 // [B + 1] first tile of each sequence
+  int *err;
+  void *out;
+  float *lse;
+};
+
+// What a sequence's length means for the decode.
+struct PagedSeq {
+  int L, jw, j_first, tiles;      // length, first visible key, first key of tile 0, tiles per (kv head, head block)
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedDecodeArgs &p, int b) {
+  PagedSeq s;
+  s.L = p.seqlens[b];
+  if (s.L < 0 || (long long)s.L > ((long long)p.max_pages << p.page_log2)) s.L = 0;  // outside the contract: no key
+  s.jw = p.window > 0 ? max(0, s.L - p.window) : 0;
+  if (p.list != nullptr) {
+    s.j_first = 0;
+    s.tiles = s.L > 0 ? (int)((((long long)p.n_list << p.page_log2) + PD_TILE - 1) / PD_TILE) : 0;
+  } else {
+    s.j_first = s.jw & ~(PD_TILE - 1);
+    s.tiles = (int)(((long long)s.L - s.j_first + PD_TILE - 1) / PD_TILE);
+  }
+  return s;
+}
+
+// First key of 16-key block `blk` of tile u, and its pool row block: the page
+// in `page` (its slot is the key index mod P).  -1: nothing to read there (past
+// the length, before the window, no such page).
+__device__ __forceinline__ int paged_block(const PagedDecodeArgs &p, const PagedSeq &s, int b, int kvh, int u, int blk,
+                                           int &page) {
+  int j0;
+  const long long at = (long long)u * PD_TILE + blk * PD_BLK;
+  if (p.list != nullptr) {
+    const long long e = at >> p.page_log2;
+    if (e >= p.n_list) return -1;
+    const int c = p.list[((long long)b * p.Hkv + kvh) * p.n_list + e];
+    if (c < 0 || c >= p.max_pages) return -1;
+    j0 = (c << p.page_log2) + (int)(at & ((1 << p.page_log2) - 1));
+  } else {
+    j0 = s.j_first + (int)at;
+  }
+  if (j0 >= s.L || j0 + PD_BLK <= s.jw) return -1;
+  page = p.table[(long long)b * p.table_stride + (j0 >> p.page_log2)];
+  if (page < 0 || page >= p.n_pages) return -1;
+  return j0;
+}
+
+// The work list: the tiles of all sequences in order (sequence, then kv head,
+// then head block, then tile), cut into equal runs, one per CTA.  A run meets
+// at most two (kv head, head block) pairs of a sequence that it does not
+// cover whole: the one it starts in and the one it ends in.  Their partial
+// results go to the CTA's two slots; pairs covered whole are finished in place.
+struct PagedRun {
+  long long base;    // first tile of sequence b
+  long long t0, t1;  // this CTA's tiles
+  int b;             // sequence of tile t0
+};
+
+// Computed by the whole block from the lengths on the device, so that a
+// captured step replays with the lengths of the moment.  CTA 0 also leaves the
+// first tile of every sequence in p.tab for the combine.
+template <int NT>
+__device__ __forceinline__ PagedRun paged_plan(const PagedDecodeArgs &p) {
+  __shared__ long long s_warp[NT / 32], s_run[2];
+  __shared__ int s_b;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pairs = p.Hkv * p.HB;
+  auto scan = [&](long long x, long long &total) {  // inclusive over the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    total = 0;
+    long long before = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) before += s_warp[w];
+      total += s_warp[w];
+    }
+    return x + before;
+  };
+  long long mine = 0, total;
+  for (int b = tid; b < p.B; b += NT) mine += (long long)paged_seq(p, b).tiles * pairs;
+  scan(mine, total);
+  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+  PagedRun r;
+  r.t0 = (long long)blockIdx.x * chunk;
+  r.t1 = r.t0 + chunk < total ? r.t0 + chunk : total;
+  if (tid == 0) s_b = -1;
+  __syncthreads();
+  long long carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += NT) {
+    const int b = b0 + tid;
+    const long long n = b < p.B ? (long long)paged_seq(p, b).tiles * pairs : 0;
+    long long sum;
+    const long long first = carry + scan(n, sum) - n;
+    if (b < p.B) {
+      if (blockIdx.x == 0) p.tab[b] = first;
+      if (r.t0 >= first && r.t0 < first + n) {
+        s_b = b;
+        s_run[0] = first;
+      }
+    }
+    carry += sum;
+    if (blockIdx.x != 0 && carry > r.t0) break;  // uniform over the block
+  }
+  if (blockIdx.x == 0 && tid == 0) p.tab[p.B] = carry;
+  __syncthreads();
+  r.b = s_b;
+  r.base = s_run[0];
+  if (r.t0 >= r.t1) r.b = -1;
+  return r;
+}
+
+cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st);
+
+// ------------------------------------------------------------------ append
+struct PagedAppendArgs {
+  const void *k, *v, *q;
+  void *k_pages, *v_pages, *summary, *q_out;
+  const int32_t *table;
+  long long table_stride;
+  const int32_t *cu, *seqlens;
+  int max_pages, page_log2, n_pages, T, max_new, Hkv, GS;
+  long long page_stride;
+};
+cudaError_t launch_paged_append(bool bf16, int D, bool rotate, const PagedAppendArgs &a, const InvFreq &inv, int batch,
+                                cudaStream_t st);
+
+// ------------------------------------------------------------------ select
+struct PagedSelectArgs {
+  const void *q, *summary;
+  const int32_t *table;
+  long long table_stride;
+  const int32_t *seqlens;
+  int B, Hkv, GS, max_pages, page_log2, n_pages, n_select, n_first, n_last;
+  long long w_pre;
+  int w0, plain;
+  int32_t *list;
+  float *score, *mx;  // [B, Hkv, max_pages]
+  double *fine;       // [B, Hkv, max_pages]
+  int32_t *amb;       // [B, Hkv, max_pages]
+};
+cudaError_t launch_paged_select(bool bf16, int D, const PagedSelectArgs &a, const InvFreq &inv, cudaStream_t st);
+
+}  // namespace jl

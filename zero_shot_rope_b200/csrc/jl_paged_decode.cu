@@ -1,0 +1,295 @@
+// Decode of one new token per sequence over a paged cache (sm_100a): the
+// CUDA-core kernel and the combine.
+//
+// The attention is jl_bifocal_decode's: with i = L - 1, G = G(L) and
+// n(p) = p - floor(p / G), key j is scored as
+//     s_j = <q, R(-(n(j) - n(i))) k_j> / sqrt(D)   for i - j >= w0  (remote)
+//     s_j = <q, k_j> / sqrt(D)                     for i - j <  w0  (local)
+// and out = softmax(s) V over the visible keys: those below L, within the
+// window if there is one, in the listed pages if there is a list.
+#include "jl_paged.cuh"
+
+namespace jl {
+
+namespace pgd {
+
+constexpr int NT = 256;
+constexpr int NW = NT / 32;
+constexpr float LN2 = 0.69314718055994531f;
+constexpr float LOG2E_F = 1.4426950408889634f;
+
+// PPL rotation pairs per lane: lane l holds elements PPL l .. PPL l + PPL - 1 of the
+// first half of a row and the same of the second
+template <typename T, int PPL>
+__device__ __forceinline__ void load_pairs(const T *row, int half, int lane, float (&a)[PPL], float (&b)[PPL]) {
+  if constexpr (PPL == 2 && sizeof(T) == 4) {
+    const float2 x = *reinterpret_cast<const float2 *>(row + 2 * lane);
+    const float2 y = *reinterpret_cast<const float2 *>(row + half + 2 * lane);
+    a[0] = x.x, a[1] = x.y, b[0] = y.x, b[1] = y.y;
+  } else if constexpr (PPL == 2) {
+    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(row + 2 * lane));
+    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(row + half + 2 * lane));
+    a[0] = x.x, a[1] = x.y, b[0] = y.x, b[1] = y.y;
+  } else {
+    a[0] = to_f(row[lane]);
+    b[0] = to_f(row[half + lane]);
+  }
+}
+
+// One warp takes 8 keys (half a 16-key block) of every tile and keeps its own
+// running maximum, sum and output; the warps are merged when the CTA leaves a
+// (sequence, kv head, head block).
+template <typename T, int D, int GP>
+__global__ void __launch_bounds__(NT)
+paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_constant__ InvFreq inv) {
+  constexpr int PPL = D / 64, HALF = D / 2, KW = 8;
+  __shared__ float red_ml[NW][GP][2];
+  __shared__ float red_o[NW][GP][D];
+  const PagedRun run = paged_plan<NT>(p);
+  if (run.b < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pairs = p.Hkv * p.HB;
+  const float scale = rsqrtf((float)D) * LOG2E_F;
+  double w[PPL];
+  float c1[PPL], s1[PPL];  // rotation by one position
+#pragma unroll
+  for (int e = 0; e < PPL; ++e) {
+    w[e] = inv.v[PPL * lane + e];
+    angle_cs(1, w[e], c1[e], s1[e]);
+  }
+
+  int b = run.b;
+  long long base = run.base, t = run.t0;
+  while (t < run.t1) {
+    const PagedSeq s = paged_seq(p, b);
+    const long long n = (long long)s.tiles * pairs;
+    if (t >= base + n) {
+      base += n;
+      ++b;
+      continue;
+    }
+    const int pair = (int)((t - base) / s.tiles), u0 = (int)((t - base) % s.tiles);
+    const int u1 = (int)(run.t1 - t < s.tiles - u0 ? u0 + (run.t1 - t) : s.tiles);
+    const int kvh = pair / p.HB, hb = pair % p.HB;
+    const int gh = min(PD_HEADS, p.GS - hb * PD_HEADS);
+    const int h0 = kvh * p.GS + hb * PD_HEADS;  // first query head
+    const int i = s.L - 1;
+    const int G = p.plain ? 1 : (int)group_size(s.L, p.w_pre);
+    const int ni = corr_n(i, G);
+    const int j_local = (int)max(0LL, (long long)s.L - (long long)p.w0);
+
+    float qa[GP][PPL], qb[GP][PPL], oa[GP][PPL], ob[GP][PPL], m[GP], l[GP];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      m[g] = -INFINITY;
+      l[g] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PPL; ++e) qa[g][e] = qb[g][e] = oa[g][e] = ob[g][e] = 0.f;
+      if (g < gh) {
+        load_pairs<T, PPL>((const T *)p.q + ((size_t)b * p.Hq + h0 + g) * D, HALF, lane, qa[g], qb[g]);
+#pragma unroll
+        for (int e = 0; e < PPL; ++e) qa[g][e] *= scale, qb[g][e] *= scale;
+      }
+    }
+
+    for (int u = u0; u < u1; ++u) {
+      int page;
+      const int jb = paged_block(p, s, b, kvh, u, warp >> 1, page);
+      if (jb < 0) continue;
+      const int j0 = jb + (warp & 1) * KW;
+      if (j0 >= s.L || j0 + KW <= s.jw) continue;
+      const size_t row0 = (size_t)page * p.page_stride +
+                          ((size_t)(j0 & ((1 << p.page_log2) - 1)) * p.Hkv + kvh) * D;
+      float ka[KW][PPL], kb[KW][PPL], va[KW][PPL], vb[KW][PPL];
+#pragma unroll
+      for (int x = 0; x < KW; ++x) {
+        if (j0 + x < s.L) {  // rows past the length may hold anything
+          load_pairs<T, PPL>((const T *)p.k + row0 + (size_t)x * p.Hkv * D, HALF, lane, ka[x], kb[x]);
+          load_pairs<T, PPL>((const T *)p.v + row0 + (size_t)x * p.Hkv * D, HALF, lane, va[x], vb[x]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PPL; ++e) ka[x][e] = kb[x][e] = va[x][e] = vb[x][e] = 0.f;
+        }
+      }
+      if (G > 1 && j0 < j_local) {
+        // the angle of the first key in 64 bits, the next ones a step of one
+        // position or none (j + 1 a multiple of G) further
+        float c[PPL], sn[PPL];
+#pragma unroll
+        for (int e = 0; e < PPL; ++e) angle_cs(corr_n(j0, G) - ni, w[e], c[e], sn[e]);
+        int rho = j0 % G;
+#pragma unroll
+        for (int x = 0; x < KW; ++x) {
+          if (j0 + x < j_local)
+#pragma unroll
+            for (int e = 0; e < PPL; ++e) rot_back(ka[x][e], kb[x][e], c[e], sn[e]);
+          if (++rho == G) {
+            rho = 0;
+          } else {
+#pragma unroll
+            for (int e = 0; e < PPL; ++e) {
+              const float cn = c[e] * c1[e] - sn[e] * s1[e];
+              sn[e] = fmaf(sn[e], c1[e], c[e] * s1[e]);
+              c[e] = cn;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        float sc[KW], top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < KW; ++x) {
+          float d = 0.f;
+#pragma unroll
+          for (int e = 0; e < PPL; ++e) d = fmaf(qa[g][e], ka[x][e], fmaf(qb[g][e], kb[x][e], d));
+          d = warp_sum(d);
+          sc[x] = (j0 + x < s.L && j0 + x >= s.jw) ? d : -INFINITY;
+          top = max_nan(top, sc[x]);
+        }
+        const float mn = max_nan(m[g], top);
+        if (mn == -INFINITY) continue;  // every score so far is -inf
+        const float f = exp2f(m[g] - mn);
+        m[g] = mn;
+        l[g] *= f;
+#pragma unroll
+        for (int e = 0; e < PPL; ++e) oa[g][e] *= f, ob[g][e] *= f;
+#pragma unroll
+        for (int x = 0; x < KW; ++x) {
+          const float pr = exp2f(sc[x] - mn);
+          l[g] += pr;
+#pragma unroll
+          for (int e = 0; e < PPL; ++e) {
+            oa[g][e] = fmaf(pr, va[x][e], oa[g][e]);
+            ob[g][e] = fmaf(pr, vb[x][e], ob[g][e]);
+          }
+        }
+      }
+    }
+
+    // merge the warps
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      if (lane == 0) red_ml[warp][g][0] = m[g], red_ml[warp][g][1] = l[g];
+#pragma unroll
+      for (int e = 0; e < PPL; ++e) {
+        red_o[warp][g][PPL * lane + e] = oa[g][e];
+        red_o[warp][g][HALF + PPL * lane + e] = ob[g][e];
+      }
+    }
+    __syncthreads();
+    const bool whole = u0 == 0 && u1 == s.tiles;
+    const size_t slot = 2 * (size_t)blockIdx.x + (u0 > 0 ? 0 : 1);
+    for (int idx = threadIdx.x; idx < gh * D; idx += NT) {
+      const int g = idx / D, d = idx % D;
+      float M = -INFINITY, L = 0.f, acc = 0.f;
+      for (int x = 0; x < NW; ++x) M = max_nan(M, red_ml[x][g][0]);
+      if (M != -INFINITY)
+        for (int x = 0; x < NW; ++x) {
+          const float f = exp2f(red_ml[x][g][0] - M);
+          L = fmaf(f, red_ml[x][g][1], L);
+          acc = fmaf(f, red_o[x][g][d], acc);
+        }
+      if (whole) {
+        const size_t bh = (size_t)b * p.Hq + h0 + g;
+        ((T *)p.out)[bh * D + d] = from_f<T>(M != -INFINITY ? acc / L : 0.f);
+        if (p.lse != nullptr && d == 0) p.lse[bh] = M != -INFINITY ? (M + log2f(L)) * LN2 : -INFINITY;
+      } else {
+        p.part_o[(slot * PD_HEADS + g) * D + d] = acc;
+        if (d == 0) {
+          p.part_ml[(slot * PD_HEADS + g) * 2] = M;
+          p.part_ml[(slot * PD_HEADS + g) * 2 + 1] = L;
+        }
+      }
+    }
+    t += u1 - u0;
+  }
+}
+
+// Joins the runs' partial results of one (kv head, head block) of a sequence,
+// or writes zeros and -inf where the sequence has no key.  Pairs that one run
+// covered whole were finished there.
+template <typename T, int D>
+__global__ void __launch_bounds__(NT)
+paged_combine_kernel(const __grid_constant__ PagedDecodeArgs p, int ctas) {
+  __shared__ float w_s[PD_MAX_CTAS][PD_HEADS];
+  __shared__ float M_s[PD_HEADS], L_s[PD_HEADS];
+  const int b = blockIdx.y, pair = blockIdx.x, pairs = p.Hkv * p.HB;
+  const int kvh = pair / p.HB, hb = pair % p.HB;
+  const int gh = min(PD_HEADS, p.GS - hb * PD_HEADS);
+  const int h0 = kvh * p.GS + hb * PD_HEADS;
+  if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *p.err = 0;
+  const long long first = p.tab[b], tiles = (p.tab[b + 1] - first) / pairs;
+  const long long total = p.tab[p.B];
+  const size_t bh0 = (size_t)b * p.Hq + h0;
+  if (tiles == 0) {
+    for (int idx = threadIdx.x; idx < gh * D; idx += NT) ((T *)p.out)[bh0 * D + idx] = from_f<T>(0.f);
+    if (p.lse != nullptr && threadIdx.x < gh) p.lse[bh0 + threadIdx.x] = -INFINITY;
+    return;
+  }
+  const long long chunk = (total + ctas - 1) / ctas;
+  const long long p0 = first + pair * tiles, p1 = p0 + tiles;
+  const int c0 = (int)(p0 / chunk), c1 = (int)((p1 - 1) / chunk);
+  if (c0 == c1) return;  // covered whole
+  const int ns = c1 - c0 + 1;
+  // the pair's first run holds it in its second slot, unless it begins there
+  auto slot = [&](int x) { return 2 * (size_t)(c0 + x) + (x == 0 ? 1 : 0); };
+  for (int idx = threadIdx.x; idx < ns * PD_HEADS; idx += NT) {
+    const int x = idx / PD_HEADS, g = idx % PD_HEADS;
+    w_s[x][g] = g < gh ? p.part_ml[(slot(x) * PD_HEADS + g) * 2] : -INFINITY;
+  }
+  __syncthreads();
+  if (threadIdx.x < PD_HEADS) {
+    const int g = threadIdx.x;
+    float M = -INFINITY;
+    for (int x = 0; x < ns; ++x) M = max_nan(M, w_s[x][g]);
+    M_s[g] = M;
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < ns * PD_HEADS; idx += NT) {
+    const int x = idx / PD_HEADS, g = idx % PD_HEADS;
+    w_s[x][g] = M_s[g] == -INFINITY ? 0.f : exp2f(w_s[x][g] - M_s[g]);
+  }
+  __syncthreads();
+  if (threadIdx.x < PD_HEADS) {
+    const int g = threadIdx.x;
+    float L = 0.f;
+    if (g < gh)
+      for (int x = 0; x < ns; ++x) L = fmaf(w_s[x][g], p.part_ml[(slot(x) * PD_HEADS + g) * 2 + 1], L);
+    L_s[g] = L;
+    if (g < gh && p.lse != nullptr) p.lse[bh0 + g] = M_s[g] == -INFINITY ? -INFINITY : (M_s[g] + log2f(L)) * LN2;
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < gh * D; idx += NT) {
+    const int g = idx / D, d = idx % D;
+    float acc = 0.f;
+#pragma unroll 4
+    for (int x = 0; x < ns; ++x) acc = fmaf(w_s[x][g], p.part_o[(slot(x) * PD_HEADS + g) * D + d], acc);
+    ((T *)p.out)[bh0 * D + idx] = from_f<T>(M_s[g] == -INFINITY ? 0.f : acc / L_s[g]);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch(const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
+  constexpr int ctas = 296;
+  const int gp = a.GS > PD_HEADS ? PD_HEADS : a.GS;
+  if (gp == 1) paged_decode_kernel<T, D, 1><<<ctas, NT, 0, st>>>(a, inv);
+  else if (gp == 2) paged_decode_kernel<T, D, 2><<<ctas, NT, 0, st>>>(a, inv);
+  else if (gp <= 4) paged_decode_kernel<T, D, 4><<<ctas, NT, 0, st>>>(a, inv);
+  else paged_decode_kernel<T, D, 8><<<ctas, NT, 0, st>>>(a, inv);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  paged_combine_kernel<T, D><<<dim3(a.Hkv * a.HB, a.B), NT, 0, st>>>(a, ctas);
+  return cudaGetLastError();
+}
+
+}  // namespace pgd
+
+cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
+  if (D == 128)
+    return bf16 ? pgd::launch<__nv_bfloat16, 128>(a, inv, st) : pgd::launch<float, 128>(a, inv, st);
+  return bf16 ? pgd::launch<__nv_bfloat16, 64>(a, inv, st) : pgd::launch<float, 64>(a, inv, st);
+}
+
+}  // namespace jl

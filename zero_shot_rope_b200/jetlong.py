@@ -21,6 +21,7 @@ JL_BF16, JL_FP32 = 0, 1
 JL_FLAG_PLAIN_CAUSAL = 0x1
 JL_FLAG_SIMT = 0x2
 JL_FLAG_PREROTATE_K = 0x4
+JL_FLAG_ROTATE = 0x8
 
 _lib = None
 
@@ -73,6 +74,20 @@ def lib() -> ctypes.CDLL:
                                             c_i64, c_i32, c_d, c_p, c_p, ctypes.c_int, c_u32, c_p]
     L.jl_bifocal_decode_noalloc_error.restype = ctypes.c_int
     L.jl_bifocal_decode_noalloc_error.argtypes = [ctypes.POINTER(c_i32), c_p]
+    L.jl_paged_append.restype = ctypes.c_int
+    L.jl_paged_append.argtypes = ([c_p] * 6 + [c_i64, c_i32, c_p, c_p] + [c_i32] * 8 +
+                                  [c_i64, c_p, c_p, c_d, ctypes.c_int, c_u32, c_p])
+    L.jl_bifocal_select_pages_workspace_size.restype = c_sz
+    L.jl_bifocal_select_pages_workspace_size.argtypes = [c_i32] * 4
+    L.jl_bifocal_select_pages.restype = ctypes.c_int
+    L.jl_bifocal_select_pages.argtypes = ([c_p] * 3 + [c_i64, c_i32, c_p] + [c_i32] * 9 +
+                                          [c_i64, c_i32, c_d, c_p, c_p, c_sz, ctypes.c_int, c_u32, c_p])
+    L.jl_bifocal_decode_paged_workspace_size.restype = c_sz
+    L.jl_bifocal_decode_paged_workspace_size.argtypes = [c_i32] * 2
+    L.jl_bifocal_decode_paged.restype = ctypes.c_int
+    L.jl_bifocal_decode_paged.argtypes = ([c_p] * 4 + [c_i64, c_i32, c_p, c_p] + [c_i32] * 7 +
+                                          [c_i64, c_i64, c_i32, c_i32, c_d, c_p, c_p, c_p, c_sz, ctypes.c_int,
+                                           c_u32, c_p])
     L.jl_debug_set_wait_limit.restype = ctypes.c_int
     L.jl_debug_set_wait_limit.argtypes = [ctypes.c_ulonglong]
     _lib = L
@@ -244,3 +259,225 @@ def jl_bifocal_decode_noalloc_error(stream=None) -> int:
     _check(lib().jl_bifocal_decode_noalloc_error(ctypes.byref(word), st))
     (stream or torch.cuda.current_stream()).synchronize()
     return int(word.value)
+
+
+# ------------------------------------------------------------- paged cache
+# The paged calls also check shapes, types, strides and devices here (the C
+# ABI sees pointers only), run on the device of their tensors whichever is
+# current, and allocate what the caller did not pass on the stream they run on.
+
+class _On:
+    """Makes ``device`` and ``stream`` current, where they are not already."""
+
+    __slots__ = ("ctx", "raw")
+
+    def __init__(self, device, stream):
+        self.ctx = None
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device (got {device})")
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, tensors on {device}")
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _tensor(name, t, shape, dtype, device):
+    """Raise unless t is a contiguous tensor of this shape (-1: any extent),
+    type and device."""
+    if tuple(t.shape) != shape and (t.dim() != len(shape) or
+                                    any(w != -1 and w != n for w, n in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {list(shape)} (got {list(t.shape)})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _pools(k_pages, v_pages, n_kv_heads, head_dim, dtype, device):
+    """(page size, pages, stride between pages) of the two pools."""
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[2:] != (n_kv_heads, head_dim):
+        raise ValueError(f"k_pages and v_pages must both be [n_pages, page_size, {n_kv_heads}, {head_dim}] "
+                         f"(got {list(k_pages.shape)}, {list(v_pages.shape)})")
+    if k_pages.dtype != dtype or v_pages.dtype != dtype:
+        raise TypeError(f"k_pages and v_pages must be {dtype} (got {k_pages.dtype}, {v_pages.dtype})")
+    if k_pages.device != device or v_pages.device != device:
+        raise ValueError(f"k_pages and v_pages must be on {device}")
+    n, page = k_pages.shape[0], k_pages.shape[1]
+    if n == 0:
+        raise ValueError("the pools have no page")
+    if k_pages.is_contiguous() and v_pages.is_contiguous():
+        return page, n, page * n_kv_heads * head_dim
+    if not (k_pages[0].is_contiguous() and v_pages[0].is_contiguous()):
+        raise ValueError("each page of k_pages and v_pages must be contiguous")
+    if n == 1:
+        return page, n, page * n_kv_heads * head_dim
+    if k_pages.stride(0) != v_pages.stride(0):
+        raise ValueError("k_pages and v_pages must have the same stride between pages")
+    return page, n, k_pages.stride(0)
+
+
+def _table(block_table, batch, device):
+    """(pages per sequence, row stride) of the block table."""
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must have shape [{batch}, max_pages] (got {list(block_table.shape)})")
+    if block_table.dtype != torch.int32:
+        raise TypeError(f"block_table must be torch.int32 (got {block_table.dtype})")
+    if block_table.device != device:
+        raise ValueError(f"block_table is on {block_table.device}, expected {device}")
+    cols = block_table.shape[1]
+    if cols > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table's rows must be contiguous")
+    return cols, (block_table.stride(0) if batch > 1 else cols)
+
+
+def _given(name, t, shape, dtype, device):
+    """t if it is fit to be written, a new tensor if there is none."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _tensor(name, t, shape, dtype, device)
+    return t
+
+
+def _scratch(workspace, nbytes, device):
+    """(tensor, pointer, bytes) of the workspace; the tensor keeps it alive."""
+    if nbytes == 0:
+        return None, None, 0
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _heads3(name, t):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions (got {list(t.shape)})")
+    return t.shape
+
+
+def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, max_new, page_summary=None, q=None,
+                    q_out=None, rope_theta=None, stream=None):
+    """Write new tokens into a paged cache: k, v [T, Hkv, D], sequence b's rows
+    cu_seqlens[b] .. cu_seqlens[b+1] - 1, the last at position seqlens[b] - 1.
+
+    With ``rope_theta`` k (and q [T, Hq, D], if given) arrive before RoPE and
+    are rotated by their positions; without it k is stored as given.
+    ``page_summary`` [n_pages, Hkv, 2, D], if given, is kept up to date.
+    Returns the rotated q (``q_out``; it may be q itself) or None."""
+    T, Hkv, D = _heads3("k", k)
+    device, dtype = k.device, k.dtype
+    code = _dtype_code(k)
+    B = seqlens.numel()
+    _tensor("k", k, (T, Hkv, D), dtype, device)
+    _tensor("v", v, (T, Hkv, D), dtype, device)
+    page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, dtype, device)
+    cols, table_stride = _table(block_table, B, device)
+    _tensor("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, device)
+    _tensor("seqlens", seqlens, (B,), torch.int32, device)
+    if page_summary is not None:
+        _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, device)
+    if rope_theta is None and q is not None:
+        raise ValueError("q is only rotated: it needs rope_theta")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    Hq = Hkv
+    if q is not None:
+        Hq = _heads3("q", q)[1]
+        _tensor("q", q, (T, Hq, D), dtype, device)
+    with _On(device, stream) as st:
+        if q is not None:
+            q_out = _given("q_out", q_out, (T, Hq, D), dtype, device)
+        _check(lib().jl_paged_append(
+            k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            None if page_summary is None else page_summary.data_ptr(), block_table.data_ptr(), table_stride, cols,
+            cu_seqlens.data_ptr(), seqlens.data_ptr(), B, T, int(max_new), Hq, Hkv, D, page, n_pages, page_stride,
+            None if q is None else q.data_ptr(), None if q is None else q_out.data_ptr(),
+            0.0 if rope_theta is None else float(rope_theta), code, 0 if rope_theta is None else JL_FLAG_ROTATE, st))
+    return q_out
+
+
+def jl_bifocal_select_pages_workspace_size(batch, n_kv_heads, max_pages, n_select) -> int:
+    return int(lib().jl_bifocal_select_pages_workspace_size(batch, n_kv_heads, max_pages, n_select))
+
+
+def jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_select, w_pretrained, w0, rope_theta,
+                            n_first=1, n_last=1, out=None, flags=0, workspace=None, stream=None):
+    """The logical pages that each new token should read: the ``n_first``
+    first, the ``n_last`` newest and the highest scored others of every kv
+    head, ascending, -1 behind the last: int32 [B, Hkv, n_select], for
+    jl_bifocal_decode_paged.  q [B, Hq, D] at position seqlens[b] - 1."""
+    B, Hq, D = _heads3("q", q)
+    device, dtype = q.device, q.dtype
+    code = _dtype_code(q)
+    if page_summary.dim() != 4:
+        raise ValueError(f"page_summary must be [n_pages, Hkv, 2, D] (got {list(page_summary.shape)})")
+    n_pages, Hkv = page_summary.shape[0], page_summary.shape[1]
+    n_select = int(n_select)
+    _tensor("q", q, (B, Hq, D), dtype, device)
+    _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, device)
+    cols, table_stride = _table(block_table, B, device)
+    _tensor("seqlens", seqlens, (B,), torch.int32, device)
+    L = lib()
+    with _On(device, stream) as st:
+        out = _given("out", out, (B, Hkv, max(n_select, 0)), torch.int32, device)
+        need = L.jl_bifocal_select_pages_workspace_size(B, Hkv, cols, n_select)
+        keep, ws, ws_bytes = _scratch(workspace, need, device)
+        _check(L.jl_bifocal_select_pages(
+            q.data_ptr(), page_summary.data_ptr(), block_table.data_ptr(), table_stride, cols, seqlens.data_ptr(),
+            B, Hq, Hkv, D, int(page_size), n_pages, n_select, int(n_first), int(n_last), int(w_pretrained), int(w0),
+            float(rope_theta), out.data_ptr(), ws, ws_bytes, code, int(flags), st))
+    return out
+
+
+def jl_bifocal_decode_paged_workspace_size(batch, head_dim) -> int:
+    return int(lib().jl_bifocal_decode_paged_workspace_size(batch, head_dim))
+
+
+def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrained, w0, rope_theta, page_list=None,
+                            window=0, out=None, lse=None, flags=0, workspace=None, stream=None):
+    """One decode step over a paged cache: q [B, Hq, D] at position
+    seqlens[b] - 1 against the pages of block_table [B, max_pages]; only those
+    of ``page_list`` [B, Hkv, n] if given, only the last ``window`` keys if
+    not 0.  Returns (out [B, Hq, D], lse [B, Hq] or None)."""
+    B, Hq, D = _heads3("q", q)
+    device, dtype = q.device, q.dtype
+    code = _dtype_code(q)
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages must be [n_pages, page_size, Hkv, D] (got {list(k_pages.shape)})")
+    Hkv = k_pages.shape[2]
+    _tensor("q", q, (B, Hq, D), dtype, device)
+    page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, dtype, device)
+    cols, table_stride = _table(block_table, B, device)
+    _tensor("seqlens", seqlens, (B,), torch.int32, device)
+    listed, n_list = None, 0
+    if page_list is not None:
+        _tensor("page_list", page_list, (B, Hkv, -1), torch.int32, device)
+        # an empty list's own pointer may be null: nothing of it is read
+        listed, n_list = page_list.data_ptr() or block_table.data_ptr(), page_list.shape[2]
+    if lse is not None:
+        _tensor("lse", lse, (B, Hq), torch.float32, device)
+    L = lib()
+    with _On(device, stream) as st:
+        out = _given("out", out, (B, Hq, D), dtype, device)
+        need = L.jl_bifocal_decode_paged_workspace_size(B, D)
+        keep, ws, ws_bytes = _scratch(workspace, need, device)
+        _check(L.jl_bifocal_decode_paged(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), table_stride, cols,
+            seqlens.data_ptr(), listed, n_list, B, Hq, Hkv, D, page, n_pages, page_stride, int(w_pretrained), int(w0),
+            int(window), float(rope_theta), out.data_ptr(), None if lse is None else lse.data_ptr(), ws, ws_bytes,
+            code, int(flags), st))
+    return out, lse
