@@ -517,3 +517,31 @@ def test_a_strided_block_table():
     ro, rl, to, tl = P.decode(q, keys, vals, 100, 40, 1e4)
     P.check(out, ro, to, "out")
     P.check(lse, rl, tl, "lse")
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_decode_returns_whatever_the_wait_limit(D):
+    # With the limit at 1 ns a wait that outlasts its first probes gives up.
+    # mbarrier.try_wait itself suspends for a time that the hardware sets, so
+    # whether one does is not for the test to say: the call must return, report
+    # 64 if one did and be right if none did, and leave the next call sound.
+    J = jl()
+    lens, page = (30000, 9000), 64
+    q = torch.randn(2, 8, D, generator=torch.Generator().manual_seed(1)).to(BF)
+    kp, vp, table, keys, vals = P.make_cache(lens, page, 2, D, BF, 5)
+    kd, vd = kp.to(DEV), vp.to(DEV)
+    ws = torch.zeros(J.jl_bifocal_decode_paged_workspace_size(2, D), dtype=torch.uint8, device=DEV)
+    assert J.lib().jl_debug_set_wait_limit(1) == 0
+    try:
+        first, _ = J.jl_bifocal_decode_paged(q.to(DEV), kd, vd, i32(table), i32(lens), 8000, 100, 1e4, workspace=ws)
+        torch.cuda.synchronize()
+        code = int(ws[:4].view(torch.int32))
+        assert code in (0, 64)
+    finally:
+        assert J.lib().jl_debug_set_wait_limit(0) == 0
+    out, lse = run_decode(q, kd, vd, table, lens, 8000, 100, 1e4)
+    ro, rl, to, tl = P.decode(q, keys, vals, 8000, 100, 1e4)
+    if code == 0:
+        P.check(first, ro, to, "out under the short limit")
+    P.check(out, ro, to, "out")
+    P.check(lse, rl, tl, "lse")

@@ -13,7 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libjetlong.so")
 SOURCES = ["jl_api.cu", "jl_simt.cu", "jl_decode.cu", "jl_decode_sm100.cu", "jl_prefill_sm100.cu",
-           "jl_paged_append.cu", "jl_paged_select.cu", "jl_paged_decode.cu"]
+           "jl_paged_append.cu", "jl_paged_select.cu", "jl_paged_decode.cu", "jl_paged_decode_sm100.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

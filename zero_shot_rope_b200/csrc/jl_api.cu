@@ -419,8 +419,8 @@ jl_status jl_bifocal_select_pages(const void *q, const void *page_summary, const
 size_t jl_bifocal_decode_paged_workspace_size(int32_t batch, int32_t head_dim) {
   if (batch <= 0 || head_dim <= 0) return 0;
   const size_t rows = (size_t)2 * jl::PD_MAX_CTAS * jl::PD_HEADS;
-  return 256 + align256(rows * head_dim * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
-         align256(((size_t)batch + 1) * sizeof(long long));
+  return 256 + align256(jl::PD_MAX_CTAS * sizeof(int)) + align256(rows * head_dim * sizeof(float)) +
+         align256(rows * 2 * sizeof(float)) + align256(((size_t)batch + 1) * sizeof(long long));
 }
 
 jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
@@ -476,7 +476,8 @@ jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void
   a.window = window;
   a.plain = (flags & JL_FLAG_PLAIN_CAUSAL) ? 1 : 0;
   a.err = (int *)workspace;
-  a.part_o = (float *)((char *)workspace + 256);
+  a.cta_err = (int *)((char *)workspace + 256);
+  a.part_o = (float *)((char *)a.cta_err + align256(jl::PD_MAX_CTAS * sizeof(int)));
   a.part_ml = (float *)((char *)a.part_o + align256(rows * head_dim * sizeof(float)));
   a.tab = (long long *)((char *)a.part_ml + align256(rows * 2 * sizeof(float)));
   a.out = out;
@@ -493,6 +494,7 @@ namespace jl {
 cudaError_t set_wait_limit_prefill(unsigned long long ns);
 cudaError_t set_wait_limit_decode_tc(unsigned long long ns);
 cudaError_t set_wait_limit_decode(unsigned long long ns);
+cudaError_t set_wait_limit_paged(unsigned long long ns);
 }  // namespace jl
 
 extern "C" int jl_debug_set_wait_limit(unsigned long long ns) {
@@ -500,6 +502,7 @@ extern "C" int jl_debug_set_wait_limit(unsigned long long ns) {
   cudaError_t e = jl::set_wait_limit_prefill(ns);
   if (e == cudaSuccess) e = jl::set_wait_limit_decode_tc(ns);
   if (e == cudaSuccess) e = jl::set_wait_limit_decode(ns);
+  if (e == cudaSuccess) e = jl::set_wait_limit_paged(ns);
   if (e != cudaSuccess) {
     fail(JL_ERR_CUDA, "setting the wait limit failed: %s", cudaGetErrorString(e));
     return -1;

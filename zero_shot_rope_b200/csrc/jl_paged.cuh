@@ -31,7 +31,7 @@ constexpr int PG_MIN_LOG2 = 4, PG_MAX_LOG2 = 8;  // page sizes 16 .. 256
 constexpr int PD_TILE = 64;
 constexpr int PD_BLK = 16;
 constexpr int PD_HEADS = 8;     // query heads a CTA serves at a time (of one kv head)
-constexpr int PD_MAX_CTAS = 296;
+constexpr int PD_MAX_CTAS = 296;  // two per SM (the CUDA-core kernel); the tensor-core kernel runs one
 
 struct PagedDecodeArgs {
   const void *q, *k, *v;          // k, v: the pools
@@ -47,7 +47,8 @@ struct PagedDecodeArgs {
   float *part_o;                  // [2 * CTAs][PD_HEADS][D]
   float *part_ml;                 // [2 * CTAs][PD_HEADS][2]
   long long *tab;                 // [B + 1] first tile of each sequence
-  int *err;
+  int *err;                       // the call's error word, and one for each CTA behind it
+  int *cta_err;
   void *out;
   float *lse;
 };
@@ -165,6 +166,9 @@ __device__ __forceinline__ PagedRun paged_plan(const PagedDecodeArgs &p) {
   return r;
 }
 
+// The tensor-core kernel (bf16): the partial results only; paged_decode_tc_ctas() runs.
+int paged_decode_tc_ctas();
+cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st);
 cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st);
 
 // ------------------------------------------------------------------ append

@@ -46,6 +46,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
   __shared__ float red_ml[NW][GP][2];
   __shared__ float red_o[NW][GP][D];
   const PagedRun run = paged_plan<NT>(p);
+  if (threadIdx.x == 0) p.cta_err[blockIdx.x] = 0;  // this kernel has no waits that could run out
   if (run.b < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pairs = p.Hkv * p.HB;
@@ -219,7 +220,12 @@ paged_combine_kernel(const __grid_constant__ PagedDecodeArgs p, int ctas) {
   const int kvh = pair / p.HB, hb = pair % p.HB;
   const int gh = min(PD_HEADS, p.GS - hb * PD_HEADS);
   const int h0 = kvh * p.GS + hb * PD_HEADS;
-  if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *p.err = 0;
+  if (blockIdx.x == 0 && b == 0 && threadIdx.x < 32) {  // fold the CTAs' error words
+    int e = 0;
+    for (int x = threadIdx.x; x < ctas; x += 32) e |= p.cta_err[x];
+    e = __reduce_or_sync(0xffffffffu, e);
+    if (threadIdx.x == 0) *p.err = e;
+  }
   const long long first = p.tab[b], tiles = (p.tab[b + 1] - first) / pairs;
   const long long total = p.tab[p.B];
   const size_t bh0 = (size_t)b * p.Hq + h0;
@@ -271,25 +277,34 @@ paged_combine_kernel(const __grid_constant__ PagedDecodeArgs p, int ctas) {
 }
 
 template <typename T, int D>
-cudaError_t launch(const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
-  constexpr int ctas = 296;
-  const int gp = a.GS > PD_HEADS ? PD_HEADS : a.GS;
-  if (gp == 1) paged_decode_kernel<T, D, 1><<<ctas, NT, 0, st>>>(a, inv);
-  else if (gp == 2) paged_decode_kernel<T, D, 2><<<ctas, NT, 0, st>>>(a, inv);
-  else if (gp <= 4) paged_decode_kernel<T, D, 4><<<ctas, NT, 0, st>>>(a, inv);
-  else paged_decode_kernel<T, D, 8><<<ctas, NT, 0, st>>>(a, inv);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+cudaError_t combine(const PagedDecodeArgs &a, int ctas, cudaStream_t st) {
   paged_combine_kernel<T, D><<<dim3(a.Hkv * a.HB, a.B), NT, 0, st>>>(a, ctas);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_fp32(const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
+  constexpr int ctas = 296;
+  const int gp = a.GS > PD_HEADS ? PD_HEADS : a.GS;
+  if (gp == 1) paged_decode_kernel<float, D, 1><<<ctas, NT, 0, st>>>(a, inv);
+  else if (gp == 2) paged_decode_kernel<float, D, 2><<<ctas, NT, 0, st>>>(a, inv);
+  else if (gp <= 4) paged_decode_kernel<float, D, 4><<<ctas, NT, 0, st>>>(a, inv);
+  else paged_decode_kernel<float, D, 8><<<ctas, NT, 0, st>>>(a, inv);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : combine<float, D>(a, ctas, st);
+}
+
+template <int D>
+cudaError_t launch_bf16(const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
+  const cudaError_t e = launch_paged_decode_tc(D, a, inv, st);
+  return e != cudaSuccess ? e : combine<__nv_bfloat16, D>(a, paged_decode_tc_ctas(), st);
 }
 
 }  // namespace pgd
 
 cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
-  if (D == 128)
-    return bf16 ? pgd::launch<__nv_bfloat16, 128>(a, inv, st) : pgd::launch<float, 128>(a, inv, st);
-  return bf16 ? pgd::launch<__nv_bfloat16, 64>(a, inv, st) : pgd::launch<float, 64>(a, inv, st);
+  if (D == 128) return bf16 ? pgd::launch_bf16<128>(a, inv, st) : pgd::launch_fp32<128>(a, inv, st);
+  return bf16 ? pgd::launch_bf16<64>(a, inv, st) : pgd::launch_fp32<64>(a, inv, st);
 }
 
 }  // namespace jl

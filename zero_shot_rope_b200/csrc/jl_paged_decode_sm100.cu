@@ -1,0 +1,546 @@
+// Decode of one new token per sequence over a paged cache in bf16 (sm_100a).
+//
+// A step reads every visible key and value once and does little with each:
+// 2 GS products per element for GS query heads, far below what the memory
+// system lets through, so the kernel is built around an unbroken stream of
+// tiles.  The GPU's whole work is one list of 64-key tiles, cut into equal
+// runs, one per SM; a CTA goes through its run with one ring of TMA stages
+// that is not drained between sequences or heads (jl_paged.cuh has the plan).
+//
+//   warp 8     producer: looks the pages of the next tiles up and loads their
+//              K and V by TMA (SWIZZLE_128B boxes of up to 64 rows; a tile of
+//              16-key pages is four boxes of each).
+//   warp 9     angles: the bifocal turn n(j0) - n(i) of each 16-key block's
+//              first key, 64-bit angles, cosine and sine per channel pair.
+//   warps 0-7  16 keys of every second tile each: scores, weights and weighted
+//              values, with the warp's own running maximum and sum; merged when
+//              the run leaves a (sequence, kv head).
+//
+// Products are m16n8k16 in registers, with the query heads as the 16 rows.
+// They need neither tensor memory nor a trip of the turned keys through shared
+// memory: a key's channel k and its partner k + D/2 sit in the same lane (the
+// operand of step kk and that of step kk + D/32), so the rotation happens on the
+// operand's own registers.  At the memory's pace a 128-key tile pair leaves an
+// SM some 2800 cycles; its 384 products take about 770 of them.
+//
+// Precision: the turned key is split into two bf16, hi + lo, and both are
+// multiplied; the eight rows that a group of up to eight heads leaves free carry
+// the low half of the softmax weights in the second product.  So neither the
+// keys nor the weights are rounded to eight bits; scores, maxima, sums and
+// outputs are fp32.
+#include "jl_paged.cuh"
+#include "jl_ptx.cuh"
+
+namespace jl {
+namespace pgt {
+
+constexpr int NCW = 8;                      // consumer warps
+constexpr int WARP_LOAD = NCW, WARP_ANGLE = NCW + 1;
+constexpr int THREADS = (NCW + 2) * 32;
+constexpr int CTAS = 148;
+constexpr int ERR_TIMEOUT = 64;
+constexpr int NBLK = PD_TILE / PD_BLK;      // 16-key blocks of a tile
+constexpr float LN2 = 0.69314718055994531f;
+
+template <int D>
+struct Geo {
+  static constexpr int HALF = D / 2;
+  static constexpr int NH = D / 64;                    // 64-channel boxes of a row
+  static constexpr int KV = PD_TILE * D * 2;           // K or V of a tile
+  static constexpr int NST = D == 128 ? 5 : 10;        // ring stages
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = NST * KV;
+  static constexpr int ANG = NBLK * HALF * 8;          // a stage's angles
+  static constexpr int OFF_ANG = 2 * NST * KV;
+  static constexpr int OFF_TAB = OFF_ANG + NST * ANG;  // turns by 0 .. 15 positions
+  static constexpr int OFF_RED = OFF_TAB + PD_BLK * HALF * 8;
+  static constexpr int RS = D + 8;                     // row stride of the merge buffer, padded against bank conflicts
+  static constexpr int SMEM = OFF_RED + NCW * PD_HEADS * RS * 4 + 1024;
+};
+static_assert(Geo<128>::SMEM <= 227 * 1024 && Geo<64>::SMEM <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void tma_load4(const CUtensorMap *map, uint64_t *bar, uint32_t dst, int c0, int c1, int c2,
+                                          int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(su32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// packed fp32 pairs: one instruction computes both lanes
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float2 bf2_f2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t f2_bf2(float2 f) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// x as hi + lo, two bf16 pairs
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+  hi = f2_bf2(x);
+  const float2 h = bf2_f2(hi);
+  lo = f2_bf2(make_float2(x.x - h.x, x.y - h.y));
+}
+
+// The run's tiles one after another, as every warp role walks them.
+struct Walk {
+  long long base, t, t1;
+  int b, pairs;
+  PagedSeq s;
+  int pair, u0, u1;  // current piece: tiles u0 .. u1 - 1 of a pair
+  __device__ __forceinline__ Walk(const PagedDecodeArgs &p, const PagedRun &r)
+      : base(r.base), t(r.t0), t1(r.t1), b(r.b), pairs(p.Hkv * p.HB) {}
+  __device__ __forceinline__ bool next(const PagedDecodeArgs &p) {
+    while (t < t1) {
+      s = paged_seq(p, b);
+      const long long n = (long long)s.tiles * pairs;
+      if (t >= base + n) {
+        base += n;
+        ++b;
+        continue;
+      }
+      pair = (int)((t - base) / s.tiles);
+      u0 = (int)((t - base) % s.tiles);
+      u1 = (int)(t1 - t < s.tiles - u0 ? u0 + (t1 - t) : s.tiles);
+      t += u1 - u0;
+      return true;
+    }
+    return false;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                       const __grid_constant__ PagedDecodeArgs p, const __grid_constant__ InvFreq inv) {
+  using GG = Geo<D>;
+  constexpr int HALF = GG::HALF, NST = GG::NST;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[NST], bar_empty[NST];
+  __shared__ int s_j0[NST][NBLK];
+  __shared__ float red_ml[NCW][PD_HEADS][2];
+  __shared__ volatile int abort_flag;
+  __shared__ int err_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = (su32(smem_raw) + 1023u) & ~1023u;
+  uint8_t *gbase = smem_raw + (sbase - su32(smem_raw));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&bar_full[s], 2);       // producer, angles
+      mbar_init(&bar_empty[s], NBLK);   // the four consumer warps of the tile
+    }
+    abort_flag = 0;
+    err_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // turns by r = 0 .. 15 positions: {cos, cos, sin, sin} of two neighbouring
+  // pairs, the 64-byte halves of odd rows swapped so that two rows meet in
+  // different banks
+  for (int idx = threadIdx.x; idx < PD_BLK * HALF; idx += THREADS) {
+    const int r = idx / HALF, k = idx % HALF;
+    float c, s;
+    angle_cs(r, inv.v[k], c, s);
+    float *to = reinterpret_cast<float *>(gbase + GG::OFF_TAB + r * HALF * 8 + (((k >> 1) * 16) ^ ((r & 1) * 64)));
+    to[k & 1] = c;
+    to[2 + (k & 1)] = s;
+  }
+  const PagedRun run = paged_plan<THREADS>(p);
+  __syncthreads();
+
+  Walk w(p, run);
+  if (run.b >= 0) {
+    if (warp == WARP_LOAD) {
+      // ======================= producer =======================
+      const int rows = min(1 << p.page_log2, PD_TILE);  // rows of a box
+      const int runs = PD_TILE / rows;                  // boxes of K (and V) per 64 channels of a tile
+      const int per = rows / PD_BLK;                    // blocks of a box
+      int it = 0;
+      bool ok = true;
+      while (ok && w.next(p)) {
+        const int kvh = w.pair / p.HB;
+        for (int u = w.u0; u < w.u1 && ok; u += 8) {
+          // lane: block lane % 4 of tile u + lane / 4
+          int page = 0, j0 = -1;
+          if (u + (lane >> 2) < w.u1) j0 = paged_block(p, w.s, w.b, kvh, u + (lane >> 2), lane & 3, page);
+          for (int x = 0; x < 8 && u + x < w.u1; ++x, ++it) {
+            const int st = it % NST;
+            if (it >= NST) ok = wait_b(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if ((lane >> 2) == x) s_j0[st][lane & 3] = j0;
+            // a box is loaded where any of its blocks is wanted
+            const unsigned want = (__ballot_sync(0xffffffffu, j0 >= 0) >> (4 * x)) & 15u;
+            int boxes = 0;
+            for (int r = 0; r < runs; ++r) boxes += ((want >> (r * per)) & ((1u << per) - 1u)) != 0;
+            __syncwarp();
+            if (lane == 0) {
+              if (boxes > 0) mbar_expect_tx(&bar_full[st], (uint32_t)(boxes * rows * D * 2 * 2));
+              else mbar_arrive(&bar_full[st]);
+            }
+            __syncwarp();
+            // lane r loads box r: the block it takes page and slot from
+            int src = 0;
+            if (lane < runs) {
+              const unsigned mine = (want >> (lane * per)) & ((1u << per) - 1u);
+              src = 4 * x + lane * per + (mine ? __ffs(mine) - 1 : 0);
+            }
+            const int bp = __shfl_sync(0xffffffffu, page, src), bj = __shfl_sync(0xffffffffu, j0, src);
+            if (lane < runs && bj >= 0) {
+              const int slot = (bj & ((1 << p.page_log2) - 1)) & ~(rows - 1);
+              const uint32_t to = sbase + st * GG::KV + lane * rows * 128;
+#pragma unroll
+              for (int h = 0; h < GG::NH; ++h) {
+                tma_load4(&mK, &bar_full[st], to + GG::OFF_K + h * (PD_TILE * 128), 64 * h, kvh, slot, bp);
+                tma_load4(&mV, &bar_full[st], to + GG::OFF_V + h * (PD_TILE * 128), 64 * h, kvh, slot, bp);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+      // after a timeout, let the loads in flight land
+      if (!ok)
+        for (int x = max(0, it - NST); x < it; ++x)
+          wait_drain(&bar_full[x % NST], (x / NST) & 1, &err_s, ERR_TIMEOUT);
+    } else if (warp == WARP_ANGLE) {
+      // ======================= angles =======================
+      int it = 0;
+      bool ok = true;
+      while (ok && w.next(p)) {
+        const int kvh = w.pair / p.HB;
+        const int G = p.plain ? 1 : (int)group_size(w.s.L, p.w_pre);
+        const int ni = corr_n(w.s.L - 1, G);
+        const int j_local = (int)max(0LL, (long long)w.s.L - (long long)p.w0);
+        for (int u = w.u0; u < w.u1 && ok; u += 8) {
+          int page, j0 = -1;
+          if (G > 1 && u + (lane >> 2) < w.u1) j0 = paged_block(p, w.s, w.b, kvh, u + (lane >> 2), lane & 3, page);
+          if (j0 >= j_local) j0 = -1;  // a local block
+          const int n = j0 >= 0 ? corr_n(j0, G) - ni : 0;
+          const unsigned want = __ballot_sync(0xffffffffu, j0 >= 0);
+          for (int x = 0; x < 8 && u + x < w.u1; ++x, ++it) {
+            const int st = it % NST;
+            if (it >= NST) ok = wait_b(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+#pragma unroll 1
+            for (int blk = 0; blk < NBLK; ++blk) {
+              if (!((want >> (4 * x + blk)) & 1u)) continue;
+              const int nb = __shfl_sync(0xffffffffu, n, 4 * x + blk);
+              float *to = reinterpret_cast<float *>(gbase + GG::OFF_ANG + st * GG::ANG + blk * HALF * 8);
+#pragma unroll
+              for (int e = 0; e < HALF / 32; ++e) {
+                const int k = lane + 32 * e;
+                float c, s;
+                angle_cs(nb, inv.v[k], c, s);
+                to[(k >> 1) * 4 + (k & 1)] = c;
+                to[(k >> 1) * 4 + 2 + (k & 1)] = s;
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_full[st]);
+          }
+        }
+      }
+    } else {
+      // ======================= consumers =======================
+      const int blk = warp & 3, par = warp >> 2;
+      const int q4 = lane & 3, row = lane >> 2;
+      const float scale = rsqrtf((float)D) * 1.4426950408889634f;
+      // ldmatrix addresses within a tile half: K [key][16-byte chunk], and V the same, transposed on the way
+      const int lm = lane >> 3, lr = lane & 7;
+      const uint32_t k_row = (uint32_t)((blk * PD_BLK + (lm >> 1) * 8 + lr) * 128);
+      const uint32_t v_row = (uint32_t)((blk * PD_BLK + (lm & 1) * 8 + lr) * 128);
+      int it = 0;
+      bool ok = true;
+      while (w.next(p)) {
+        const int kvh = w.pair / p.HB, hb = w.pair % p.HB;
+        const int gh = min(PD_HEADS, p.GS - hb * PD_HEADS);
+        const int h0 = kvh * p.GS + hb * PD_HEADS;
+        const int L = w.s.L, jw = w.s.jw;
+        const int G = p.plain ? 1 : (int)group_size(L, p.w_pre);
+        const int j_local = G > 1 ? (int)max(0LL, (long long)L - (long long)p.w0) : 0;
+        // query operand: row = head, channels 16 x + 2 q4 + {0, 1} and + 8
+        uint32_t qf[D / 16][2];
+        {
+          const uint32_t *q = reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)p.q +
+                                                                 ((size_t)w.b * p.Hq + h0 + row) * D);
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            qf[x][0] = row < gh ? q[8 * x + q4] : 0u;
+            qf[x][1] = row < gh ? q[8 * x + 4 + q4] : 0u;
+          }
+        }
+        float o[D / 8][4], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+
+        for (int u = w.u0; u < w.u1; ++u, ++it) {
+          if ((it & 1) != par) continue;
+          const int st = it % NST;
+          if (ok) ok = wait_b(&bar_full[st], (it / NST) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;  // the run is walked to its end, so that the merges' barriers are met
+          const int j0 = s_j0[st][blk];
+          if (j0 >= 0) {
+            const uint32_t kt = sbase + GG::OFF_K + st * GG::KV + k_row;
+            const uint32_t vt = sbase + GG::OFF_V + st * GG::KV + v_row;
+            // scores of keys 8 nb + 2 q4 + {0, 1} for head `row` in c[nb][0..1]
+            float sc[2][2];
+            auto plain_scores = [&]() {
+              float c[2][4] = {};
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x) {
+                uint32_t kf[4];
+                ldsm4(kt + (x >> 2) * (PD_TILE * 128) + ((((x & 3) * 2 + (lm & 1)) ^ lr) << 4), kf);
+                mma(c[0], qf[x][0], 0u, qf[x][1], 0u, kf[0], kf[1]);
+                mma(c[1], qf[x][0], 0u, qf[x][1], 0u, kf[2], kf[3]);
+              }
+              sc[0][0] = c[0][0], sc[0][1] = c[0][1], sc[1][0] = c[1][0], sc[1][1] = c[1][1];
+            };
+            if (j0 >= j_local) {
+              plain_scores();
+            } else {
+              // positions by which this lane's two keys (row and row + 8) turn beyond the block's first
+              const int nj = corr_n(j0, G);
+              const int r0 = corr_n(j0 + row, G) - nj, r1 = corr_n(j0 + 8 + row, G) - nj;
+              const uint32_t ang = sbase + GG::OFF_ANG + st * GG::ANG + blk * HALF * 8 + q4 * 16;
+              const uint32_t tab = sbase + GG::OFF_TAB;
+              const uint32_t t0 = tab + r0 * HALF * 8, t1 = tab + r1 * HALF * 8;
+              const uint32_t x0 = (r0 & 1) * 64, x1 = (r1 & 1) * 64;
+              float c[2][4] = {}, cl[2][4] = {};
+#pragma unroll
+              for (int x = 0; x < D / 32; ++x) {
+                // channels 16 x .. + 15 and their partners
+                uint32_t ka[4], kb[4];
+                ldsm4(kt + (((x * 2 + (lm & 1)) ^ lr) << 4), ka);
+                if constexpr (D == 128)
+                  ldsm4(kt + PD_TILE * 128 + (((x * 2 + (lm & 1)) ^ lr) << 4), kb);
+                else
+                  ldsm4(kt + (((4 + x * 2 + (lm & 1)) ^ lr) << 4), kb);
+                uint32_t ah[4], al[4], bh[4], bl[4];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {  // channels + 8 y
+                  const uint32_t at = (x * 16 + y * 8) * 8;
+                  const float4 f = lds_f4(ang + at);
+                  const float2 fc = make_float2(f.x, f.y), fs = make_float2(f.z, f.w);
+#pragma unroll
+                  for (int nb = 0; nb < 2; ++nb) {
+                    const float4 g = lds_f4((nb ? t1 : t0) + ((at + q4 * 16) ^ (nb ? x1 : x0)));
+                    const float2 gc = make_float2(g.x, g.y), gs = make_float2(g.z, g.w);
+                    const float2 co = fma2(fc, gc, neg2(mul2(fs, gs)));
+                    const float2 si = fma2(fs, gc, mul2(fc, gs));
+                    const float2 a = bf2_f2(ka[2 * nb + y]), b = bf2_f2(kb[2 * nb + y]);
+                    split2(fma2(a, co, mul2(b, si)), ah[2 * nb + y], al[2 * nb + y]);
+                    split2(fma2(b, co, neg2(mul2(a, si))), bh[2 * nb + y], bl[2 * nb + y]);
+                  }
+                }
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb) {
+                  mma(c[nb], qf[x][0], 0u, qf[x][1], 0u, ah[2 * nb], ah[2 * nb + 1]);
+                  mma(cl[nb], qf[x][0], 0u, qf[x][1], 0u, al[2 * nb], al[2 * nb + 1]);
+                  mma(c[nb], qf[D / 32 + x][0], 0u, qf[D / 32 + x][1], 0u, bh[2 * nb], bh[2 * nb + 1]);
+                  mma(cl[nb], qf[D / 32 + x][0], 0u, qf[D / 32 + x][1], 0u, bl[2 * nb], bl[2 * nb + 1]);
+                }
+              }
+              float rot[2][2];
+#pragma unroll
+              for (int nb = 0; nb < 2; ++nb) rot[nb][0] = c[nb][0] + cl[nb][0], rot[nb][1] = c[nb][1] + cl[nb][1];
+              if (j0 + PD_BLK > j_local) {  // the one block with keys of both kinds
+                plain_scores();
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (j0 + 8 * nb + 2 * q4 + e < j_local) sc[nb][e] = rot[nb][e];
+              } else {
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb) sc[nb][0] = rot[nb][0], sc[nb][1] = rot[nb][1];
+              }
+            }
+            // mask, in units of log2 e
+            const bool part = j0 + PD_BLK > L || j0 < jw;
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                sc[nb][e] *= scale;
+                if (part) {
+                  const int j = j0 + 8 * nb + 2 * q4 + e;
+                  if (j >= L || j < jw) {
+                    sc[nb][e] = -INFINITY;
+                    keep[nb] &= e == 0 ? 0xffff0000u : 0x0000ffffu;
+                  }
+                }
+              }
+            float top = max_nan(max_nan(sc[0][0], sc[0][1]), max_nan(sc[1][0], sc[1][1]));
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the maximum is only moved when it has grown by more than 2^8
+            const bool grow = !(top <= m + 8.f) && !(top == -INFINITY);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
+              if (grow) m = top;
+              l *= f;
+#pragma unroll
+              for (int x = 0; x < D / 8; ++x) o[x][0] *= f, o[x][1] *= f, o[x][2] *= f, o[x][3] *= f;
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+            uint32_t ph[2], pl[2];
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+              const float2 e = make_float2(ex2(sc[nb][0] - mu), ex2(sc[nb][1] - mu));
+              l += e.x + e.y;
+              split2(e, ph[nb], pl[nb]);
+            }
+            // rows 0-7: the weights' high halves, rows 8-15: their low halves
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              uint32_t vf[4];
+              ldsm4t(vt + (x >> 2) * (PD_TILE * 128) + ((((x & 3) * 2 + (lm >> 1)) ^ lr) << 4), vf);
+              if (part) {  // rows past the length may hold anything, and 0 NaN is NaN
+                vf[0] &= keep[0], vf[2] &= keep[0];
+                vf[1] &= keep[1], vf[3] &= keep[1];
+              }
+              mma(o[2 * x], ph[0], pl[0], ph[1], pl[1], vf[0], vf[1]);
+              mma(o[2 * x + 1], ph[0], pl[0], ph[1], pl[1], vf[2], vf[3]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_empty[st]);
+        }
+
+        // merge the warps' results of this piece
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (q4 == 0) red_ml[warp][row][0] = m, red_ml[warp][row][1] = l;
+        float *red = reinterpret_cast<float *>(gbase + GG::OFF_RED);
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+          *reinterpret_cast<float2 *>(red + (warp * PD_HEADS + row) * GG::RS + 8 * x + 2 * q4) =
+              make_float2(o[x][0] + o[x][2], o[x][1] + o[x][3]);
+        asm volatile("bar.sync 1, %0;" ::"n"(NCW * 32) : "memory");
+        const bool whole = w.u0 == 0 && w.u1 == w.s.tiles;
+        const size_t slot = 2 * (size_t)blockIdx.x + (w.u0 > 0 ? 0 : 1);
+        for (int idx = threadIdx.x; idx < gh * (D / 2); idx += NCW * 32) {
+          const int g = idx / (D / 2), d = idx % (D / 2) * 2;
+          float M = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < NCW; ++x) M = max_nan(M, red_ml[x][g][0]);
+          float sum = 0.f;
+          float2 acc = make_float2(0.f, 0.f);
+          if (M != -INFINITY)
+#pragma unroll
+            for (int x = 0; x < NCW; ++x) {
+              const float f = exp2f(red_ml[x][g][0] - M);
+              const float2 y = *reinterpret_cast<const float2 *>(red + (x * PD_HEADS + g) * GG::RS + d);
+              sum = fmaf(f, red_ml[x][g][1], sum);
+              acc.x = fmaf(f, y.x, acc.x);
+              acc.y = fmaf(f, y.y, acc.y);
+            }
+          if (whole) {
+            const size_t bh = (size_t)w.b * p.Hq + h0 + g;
+            const float r = M != -INFINITY ? 1.f / sum : 0.f;
+            reinterpret_cast<uint32_t *>(p.out)[(bh * D + d) / 2] = f2_bf2(make_float2(acc.x * r, acc.y * r));
+            if (p.lse != nullptr && d == 0) p.lse[bh] = M != -INFINITY ? (M + log2f(sum)) * LN2 : -INFINITY;
+          } else {
+            *reinterpret_cast<float2 *>(p.part_o + (slot * PD_HEADS + g) * D + d) = acc;
+            if (d == 0) {
+              p.part_ml[(slot * PD_HEADS + g) * 2] = M;
+              p.part_ml[(slot * PD_HEADS + g) * 2 + 1] = sum;
+            }
+          }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(NCW * 32) : "memory");
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) p.cta_err[blockIdx.x] = err_s;
+}
+
+static bool make_pool_map(CUtensorMap *m, const void *base, const PagedDecodeArgs &a, int D) {
+  // a pool viewed as (d, head, slot, page)
+  static EncodeTiledFn enc = get_encode_tiled();
+  if (enc == nullptr) return false;
+  const int P = 1 << a.page_log2;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hkv, (cuuint64_t)P, (cuuint64_t)a.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hkv * D * 2, (cuuint64_t)a.page_stride * 2};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)(P < PD_TILE ? P : PD_TILE), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace pgt
+
+int paged_decode_tc_ctas() { return pgt::CTAS; }
+
+cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
+  CUtensorMap mK, mV;
+  if (!pgt::make_pool_map(&mK, a.k, a, D) || !pgt::make_pool_map(&mV, a.v, a, D)) return cudaErrorInvalidValue;
+  cudaError_t e;
+  if (D == 128) {
+    e = cudaFuncSetAttribute(pgt::paged_decode_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             pgt::Geo<128>::SMEM);
+    if (e != cudaSuccess) return e;
+    pgt::paged_decode_tc_kernel<128><<<pgt::CTAS, pgt::THREADS, pgt::Geo<128>::SMEM, st>>>(mK, mV, a, inv);
+  } else {
+    e = cudaFuncSetAttribute(pgt::paged_decode_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             pgt::Geo<64>::SMEM);
+    if (e != cudaSuccess) return e;
+    pgt::paged_decode_tc_kernel<64><<<pgt::CTAS, pgt::THREADS, pgt::Geo<64>::SMEM, st>>>(mK, mV, a, inv);
+  }
+  return cudaGetLastError();
+}
+
+// Test hook: the limit of the bounded waits of this file's kernels.
+cudaError_t set_wait_limit_paged(unsigned long long ns) {
+  return cudaMemcpyToSymbol(g_wait_limit_ns, &ns, sizeof(ns));
+}
+
+}  // namespace jl
