@@ -545,3 +545,28 @@ def test_decode_returns_whatever_the_wait_limit(D):
         P.check(first, ro, to, "out under the short limit")
     P.check(out, ro, to, "out")
     P.check(lse, rl, tl, "lse")
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 16)])
+def test_decode_at_full_pace_repeats(D, page):
+    # no key is turned (G = 1), so the tiles pass at the memory's pace and their
+    # loads land out of order: many calls, all alike and right
+    J = jl()
+    lens = (65536, 31000)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    n = [-(-x // page) for x in lens]
+    kp = torch.randn(sum(n), page, 2, D, generator=g, device=DEV).to(BF)
+    vp = torch.randn(sum(n), page, 2, D, generator=g, device=DEV).to(BF)
+    order = torch.randperm(sum(n), generator=g, device=DEV).to(torch.int32)
+    table = torch.zeros(2, max(n), dtype=torch.int32, device=DEV)
+    table[0, :n[0]], table[1, :n[1]] = order[:n[0]], order[n[0]:]
+    q = torch.randn(2, 8, D, generator=g, device=DEV).to(BF)
+    out, lse = run_decode(q, kp, vp, table, lens, 1 << 20, 64, 1e4)
+    keys, vals = [[x[table[b, :n[b]].long()].reshape(-1, 2, D)[:lens[b]].cpu() for b in range(2)] for x in (kp, vp)]
+    ro, rl, to, tl = P.decode(q, keys, vals, 1 << 20, 64, 1e4)
+    P.check(out, ro, to, "out")
+    P.check(lse, rl, tl, "lse")
+    ld = i32(lens)
+    for _ in range(200):
+        again, _ = J.jl_bifocal_decode_paged(q, kp, vp, table, ld, 1 << 20, 64, 1e4)
+    assert torch.equal(again, out)

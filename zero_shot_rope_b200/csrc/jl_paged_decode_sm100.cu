@@ -47,7 +47,12 @@ struct Geo {
   static constexpr int HALF = D / 2;
   static constexpr int NH = D / 64;                    // 64-channel boxes of a row
   static constexpr int KV = PD_TILE * D * 2;           // K or V of a tile
-  static constexpr int NST = D == 128 ? 5 : 10;        // ring stages
+  // Ring stages: an even number, so that a stage's tiles all go to the same four
+  // consumer warps.  (With an odd one the two groups take turns on a stage, a
+  // group sees every second phase of its barrier only, and the parity it waits
+  // for is already true while the other group's load is still under way.)
+  static constexpr int NST = D == 128 ? 4 : 10;
+  static_assert(NST % 2 == 0, "a stage belongs to one consumer group");
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = NST * KV;
   static constexpr int ANG = NBLK * HALF * 8;          // a stage's angles
