@@ -64,6 +64,13 @@ int jl_debug_set_wait_limit(unsigned long long ns);
  */
 void jl_debug_angle_cs(int32_t n, double inv_freq, float *c, float *s);
 
+/*
+ * jl_debug_turn_cs — the paged-cache kernels' angle on the host: cos and sin
+ * of n * inv_freq through the integer product of n and the frequency in
+ * fractions of a turn.  Host-only; no CUDA call.
+ */
+void jl_debug_turn_cs(int32_t n, double inv_freq, float *c, float *s);
+
 #ifdef __cplusplus
 }
 #endif

@@ -246,3 +246,27 @@ def test_plain_forms_agree_with_the_oracle():
     assert np.abs(a - b).max() == 0.0
     x = np.random.default_rng(0).normal(size=(5, 64))
     assert np.abs(P.rotate(P.rotate(x, np.full(5, 9), 1e4), np.full(5, -9), 1e4) - x).max() < 1e-14
+
+
+def test_turns_match_64_bit_angles():
+    # cos and sin within 3 steps of 2^-24 for every position and frequency, the
+    # frequencies of a base below 1 and the largest positions among them; the
+    # angle itself is known to n w 2^-53 (the frequency is a double)
+    jl = _lib()
+    L = jl.lib()
+    L.jl_debug_turn_cs.argtypes = [ctypes.c_int32, ctypes.c_double, ctypes.POINTER(ctypes.c_float),
+                                   ctypes.POINTER(ctypes.c_float)]
+    c, s = ctypes.c_float(), ctypes.c_float()
+    rng = np.random.default_rng(1)
+    worst = 0.0
+    for theta in (1e4, 1e6, 0.5):
+        for k in range(64):
+            w = theta ** (-2.0 * k / 128)
+            for n in [0, 1, -1, 2, 16, -131071, 131071, 2 ** 30] + rng.integers(-2 ** 20, 2 ** 20, 60).tolist():
+                L.jl_debug_turn_cs(int(n), w, ctypes.byref(c), ctypes.byref(s))
+                slack = 3 * 2.0 ** -24 + 4 * abs(n) * w * 2.0 ** -53
+                err = max(abs(c.value - np.cos(n * w)), abs(s.value - np.sin(n * w)))
+                worst = max(worst, err / slack)
+    assert worst <= 1.0, worst
+    L.jl_debug_turn_cs(0, 1.0, ctypes.byref(c), ctypes.byref(s))
+    assert c.value == 1.0 and s.value == 0.0

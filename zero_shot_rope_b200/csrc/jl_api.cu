@@ -62,6 +62,16 @@ jl::InvFreq make_inv_freq(int D, double theta) {
   return f;
 }
 
+// The same frequencies in turns per position, times 2^64 (modulo a turn).
+jl::TurnFreq make_turn_freq(const jl::InvFreq &inv) {
+  jl::TurnFreq f;
+  for (int k = 0; k < JL_MAX_HALF; ++k) {
+    const double t = inv.v[k] * 0.15915494309189533577;  // 1 / (2 pi)
+    f.v[k] = (unsigned long long)std::ldexp(t - std::floor(t), 64);
+  }
+  return f;
+}
+
 jl_status check_heads(int32_t Hq, int32_t Hkv, int32_t D) {
   if (Hq <= 0 || Hkv <= 0) return fail(JL_ERR_INVALID_ARG, "head counts must be positive (Hq=%d, Hkv=%d)", Hq, Hkv);
   if (Hq % Hkv != 0) return fail(JL_ERR_INVALID_ARG, "n_q_heads (%d) is not a multiple of n_kv_heads (%d)", Hq, Hkv);
@@ -483,7 +493,7 @@ jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void
   a.out = out;
   a.lse = lse;
   const jl::InvFreq inv = make_inv_freq(head_dim, rope_theta);
-  const cudaError_t e = jl::launch_paged_decode(dtype == JL_BF16, head_dim, a, inv, (cudaStream_t)stream);
+  const cudaError_t e = jl::launch_paged_decode(dtype == JL_BF16, head_dim, a, inv, make_turn_freq(inv), (cudaStream_t)stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "paged decode launch");
 }
 
@@ -512,4 +522,10 @@ extern "C" int jl_debug_set_wait_limit(unsigned long long ns) {
 
 extern "C" void jl_debug_angle_cs(int32_t n, double inv_freq, float *c, float *s) {
   jl::angle_cs(n, inv_freq, *c, *s);
+}
+
+extern "C" void jl_debug_turn_cs(int32_t n, double inv_freq, float *c, float *s) {
+  jl::InvFreq inv = {};
+  inv.v[0] = inv_freq;
+  jl::turn_cs(n, make_turn_freq(inv).v[0], *c, *s);
 }

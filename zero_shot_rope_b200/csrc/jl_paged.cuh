@@ -23,6 +23,43 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Rotation frequencies in turns per position, as fractions of 2^64: the angle
+// of n positions, modulo a turn, is one integer product, which wraps where the
+// angle does.
+struct TurnFreq {
+  unsigned long long v[JL_MAX_HALF];
+};
+
+// cos and sin of n positions' angle.  The product's two top bits (rounded) are
+// the quadrant, the rest an angle within an eighth of a turn, whose sine and
+// cosine are the Taylor series in fp32 (to r^9 and r^10: truncated at 2e-9 and
+// 2e-10).  Off by less than 3 2^-24; about 25 instructions, against some 60 of
+// 64-bit arithmetic in angle_cs.
+__host__ __device__ __forceinline__ void turn_cs(int32_t n, unsigned long long w, float &c, float &s) {
+  const unsigned long long x = (unsigned long long)(long long)n * w;
+  const uint32_t t = (uint32_t)(x >> 32);
+  const uint32_t quad = t + 0x20000000u;              // nearest quarter turn, in the two top bits
+  const int32_t f = (int32_t)(t - (quad & 0xc0000000u));  // the rest: -2^29 .. 2^29 - 1
+  const float r = (float)f * 1.46291807926715968105e-9f;  // 2 pi / 2^32
+  const float r2 = r * r;
+  float ps = 2.7557319223985893e-6f;  // 1/9!
+  ps = fmaf(ps, r2, -1.9841269841269841e-4f);
+  ps = fmaf(ps, r2, 8.3333333333333333e-3f);
+  ps = fmaf(ps, r2, -1.6666666666666667e-1f);
+  const float sr = fmaf(r * r2, ps, r);
+  float pc = -2.7557319223985888e-7f;  // -1/10!
+  pc = fmaf(pc, r2, 2.4801587301587302e-5f);
+  pc = fmaf(pc, r2, -1.3888888888888889e-3f);
+  pc = fmaf(pc, r2, 4.1666666666666667e-2f);
+  pc = fmaf(pc, r2, -0.5f);
+  const float cr = fmaf(pc, r2, 1.f);
+  const bool swap = quad & 0x40000000u;
+  const float a = swap ? sr : cr, b = swap ? cr : sr;
+  // quadrants 0..3: (cr, sr), (-sr, cr), (-cr, -sr), (sr, -cr)
+  c = ((quad >> 30) + 1) & 2 ? -a : a;
+  s = quad & 0x80000000u ? -b : b;
+}
+
 constexpr int PG_MIN_LOG2 = 4, PG_MAX_LOG2 = 8;  // page sizes 16 .. 256
 
 // ------------------------------------------------------------------ decode
@@ -168,8 +205,8 @@ __device__ __forceinline__ PagedRun paged_plan(const PagedDecodeArgs &p) {
 
 // The tensor-core kernel (bf16): the partial results only; paged_decode_tc_ctas() runs.
 int paged_decode_tc_ctas();
-cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st);
-cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st);
+cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const TurnFreq &turn, cudaStream_t st);
+cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, const TurnFreq &turn, cudaStream_t st);
 
 // ------------------------------------------------------------------ append
 struct PagedAppendArgs {

@@ -295,16 +295,17 @@ cudaError_t launch_fp32(const PagedDecodeArgs &a, const InvFreq &inv, cudaStream
 }
 
 template <int D>
-cudaError_t launch_bf16(const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
-  const cudaError_t e = launch_paged_decode_tc(D, a, inv, st);
+cudaError_t launch_bf16(const PagedDecodeArgs &a, const TurnFreq &turn, cudaStream_t st) {
+  const cudaError_t e = launch_paged_decode_tc(D, a, turn, st);
   return e != cudaSuccess ? e : combine<__nv_bfloat16, D>(a, paged_decode_tc_ctas(), st);
 }
 
 }  // namespace pgd
 
-cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
-  if (D == 128) return bf16 ? pgd::launch_bf16<128>(a, inv, st) : pgd::launch_fp32<128>(a, inv, st);
-  return bf16 ? pgd::launch_bf16<64>(a, inv, st) : pgd::launch_fp32<64>(a, inv, st);
+cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, const TurnFreq &turn,
+                                cudaStream_t st) {
+  if (D == 128) return bf16 ? pgd::launch_bf16<128>(a, turn, st) : pgd::launch_fp32<128>(a, inv, st);
+  return bf16 ? pgd::launch_bf16<64>(a, turn, st) : pgd::launch_fp32<64>(a, inv, st);
 }
 
 }  // namespace jl

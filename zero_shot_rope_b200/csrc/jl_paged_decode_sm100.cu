@@ -11,7 +11,7 @@
 //              K and V by TMA (SWIZZLE_128B boxes of up to 64 rows; a tile of
 //              16-key pages is four boxes of each).
 //   warp 9     angles: the bifocal turn n(j0) - n(i) of each 16-key block's
-//              first key, 64-bit angles, cosine and sine per channel pair.
+//              first key: cosine and sine per channel pair.
 //   warps 0-7  16 keys of every second tile each: scores, weights and weighted
 //              values, with the warp's own running maximum and sum; merged when
 //              the run leaves a (sequence, kv head).
@@ -159,7 +159,7 @@ struct Walk {
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
 paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                       const __grid_constant__ PagedDecodeArgs p, const __grid_constant__ InvFreq inv) {
+                       const __grid_constant__ PagedDecodeArgs p, const __grid_constant__ TurnFreq turn) {
   using GG = Geo<D>;
   constexpr int HALF = GG::HALF, NST = GG::NST;
   extern __shared__ uint8_t smem_raw[];
@@ -187,7 +187,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
   for (int idx = threadIdx.x; idx < PD_BLK * HALF; idx += THREADS) {
     const int r = idx / HALF, k = idx % HALF;
     float c, s;
-    angle_cs(r, inv.v[k], c, s);
+    turn_cs(r, turn.v[k], c, s);
     float *to = reinterpret_cast<float *>(gbase + GG::OFF_TAB + r * HALF * 8 + (((k >> 1) * 16) ^ ((r & 1) * 64)));
     to[k & 1] = c;
     to[2 + (k & 1)] = s;
@@ -270,7 +270,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             if (it >= NST) ok = wait_b(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-#pragma unroll 1
+#pragma unroll
             for (int blk = 0; blk < NBLK; ++blk) {
               if (!((want >> (4 * x + blk)) & 1u)) continue;
               const int nb = __shfl_sync(0xffffffffu, n, 4 * x + blk);
@@ -279,7 +279,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
               for (int e = 0; e < HALF / 32; ++e) {
                 const int k = lane + 32 * e;
                 float c, s;
-                angle_cs(nb, inv.v[k], c, s);
+                turn_cs(nb, turn.v[k], c, s);
                 to[(k >> 1) * 4 + (k & 1)] = c;
                 to[(k >> 1) * 4 + 2 + (k & 1)] = s;
               }
@@ -525,7 +525,7 @@ static bool make_pool_map(CUtensorMap *m, const void *base, const PagedDecodeArg
 
 int paged_decode_tc_ctas() { return pgt::CTAS; }
 
-cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
+cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const TurnFreq &turn, cudaStream_t st) {
   CUtensorMap mK, mV;
   if (!pgt::make_pool_map(&mK, a.k, a, D) || !pgt::make_pool_map(&mV, a.v, a, D)) return cudaErrorInvalidValue;
   cudaError_t e;
@@ -533,12 +533,12 @@ cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const InvFre
     e = cudaFuncSetAttribute(pgt::paged_decode_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              pgt::Geo<128>::SMEM);
     if (e != cudaSuccess) return e;
-    pgt::paged_decode_tc_kernel<128><<<pgt::CTAS, pgt::THREADS, pgt::Geo<128>::SMEM, st>>>(mK, mV, a, inv);
+    pgt::paged_decode_tc_kernel<128><<<pgt::CTAS, pgt::THREADS, pgt::Geo<128>::SMEM, st>>>(mK, mV, a, turn);
   } else {
     e = cudaFuncSetAttribute(pgt::paged_decode_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              pgt::Geo<64>::SMEM);
     if (e != cudaSuccess) return e;
-    pgt::paged_decode_tc_kernel<64><<<pgt::CTAS, pgt::THREADS, pgt::Geo<64>::SMEM, st>>>(mK, mV, a, inv);
+    pgt::paged_decode_tc_kernel<64><<<pgt::CTAS, pgt::THREADS, pgt::Geo<64>::SMEM, st>>>(mK, mV, a, turn);
   }
   return cudaGetLastError();
 }
