@@ -10,7 +10,7 @@
 //   warp 8     producer: looks the pages of the next tiles up and loads their
 //              K and V by TMA (SWIZZLE_128B boxes of up to 64 rows; a tile of
 //              16-key pages is four boxes of each).
-//   warp 9     angles: the bifocal turn n(j0) - n(i) of each 16-key block's
+//   warps 9-10 angles: the bifocal turn n(j0) - n(i) of each 16-key block's
 //              first key: cosine and sine per channel pair.
 //   warps 0-7  16 keys of every second tile each: scores, weights and weighted
 //              values, with the warp's own running maximum and sum; merged when
@@ -36,7 +36,7 @@ namespace pgt {
 
 constexpr int NCW = 8;                      // consumer warps
 constexpr int WARP_LOAD = NCW, WARP_ANGLE = NCW + 1;
-constexpr int THREADS = (NCW + 2) * 32;
+constexpr int THREADS = (NCW + 3) * 32;
 constexpr int CTAS = 148;
 constexpr int ERR_TIMEOUT = 64;
 constexpr int NBLK = PD_TILE / PD_BLK;      // 16-key blocks of a tile
@@ -250,8 +250,11 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       if (!ok)
         for (int x = max(0, it - NST); x < it; ++x)
           wait_drain(&bar_full[x % NST], (x / NST) & 1, &err_s, ERR_TIMEOUT);
-    } else if (warp == WARP_ANGLE) {
+    } else if (warp >= WARP_ANGLE) {
       // ======================= angles =======================
+      // one warp per consumer group (so that it too sees every phase of its
+      // stages); the angles are formed before the stage is free for them
+      const int par = warp - WARP_ANGLE;
       int it = 0;
       bool ok = true;
       while (ok && w.next(p)) {
@@ -266,23 +269,32 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           const int n = j0 >= 0 ? corr_n(j0, G) - ni : 0;
           const unsigned want = __ballot_sync(0xffffffffu, j0 >= 0);
           for (int x = 0; x < 8 && u + x < w.u1; ++x, ++it) {
+            if ((it & 1) != par) continue;
             const int st = it % NST;
+            const bool any = (want >> (4 * x)) & 15u;
+            float c[NBLK][HALF / 32], s[NBLK][HALF / 32];
+            if (any) {
+#pragma unroll
+              for (int blk = 0; blk < NBLK; ++blk) {
+                const int nb = __shfl_sync(0xffffffffu, n, 4 * x + blk);
+#pragma unroll
+                for (int e = 0; e < HALF / 32; ++e) turn_cs(nb, turn.v[lane + 32 * e], c[blk][e], s[blk][e]);
+              }
+            }
             if (it >= NST) ok = wait_b(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            if (any) {
 #pragma unroll
-            for (int blk = 0; blk < NBLK; ++blk) {
-              if (!((want >> (4 * x + blk)) & 1u)) continue;
-              const int nb = __shfl_sync(0xffffffffu, n, 4 * x + blk);
-              float *to = reinterpret_cast<float *>(gbase + GG::OFF_ANG + st * GG::ANG + blk * HALF * 8);
+              for (int blk = 0; blk < NBLK; ++blk)
 #pragma unroll
-              for (int e = 0; e < HALF / 32; ++e) {
-                const int k = lane + 32 * e;
-                float c, s;
-                turn_cs(nb, turn.v[k], c, s);
-                to[(k >> 1) * 4 + (k & 1)] = c;
-                to[(k >> 1) * 4 + 2 + (k & 1)] = s;
-              }
+                for (int e = 0; e < HALF / 32; ++e) {
+                  const int k = lane + 32 * e;
+                  float *to = reinterpret_cast<float *>(gbase + GG::OFF_ANG + st * GG::ANG + blk * HALF * 8) +
+                              (k >> 1) * 4 + (k & 1);
+                  to[0] = c[blk][e];
+                  to[2] = s[blk][e];
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_full[st]);
