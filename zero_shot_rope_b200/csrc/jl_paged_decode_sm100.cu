@@ -82,10 +82,8 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a));
 }
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-  return v;
+__device__ __forceinline__ void lds_u64x2(uint32_t a, uint64_t &x, uint64_t &y) {
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -95,38 +93,42 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// packed fp32 pairs: one instruction computes both lanes
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+// Packed fp32 pairs, kept as 64-bit registers from the load to the last use:
+// one instruction computes both lanes.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
-__device__ __forceinline__ float2 bf2_f2(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
-__device__ __forceinline__ uint32_t f2_bf2(float2 f) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t *>(&h);
+__device__ __forceinline__ uint64_t bf2_f2(uint32_t w) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(w << 16), "r"(w & 0xffff0000u));
+  return d;
+}
+__device__ __forceinline__ uint32_t f2_bf2(uint64_t f) {
+  uint32_t d;
+  asm("{\n\t.reg .f32 x, y;\n\tmov.b64 {x, y}, %1;\n\tcvt.rn.bf16x2.f32 %0, y, x;\n\t}" : "=r"(d) : "l"(f));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
 }
 // x as hi + lo, two bf16 pairs
-__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+__device__ __forceinline__ void split2(uint64_t x, uint32_t &hi, uint32_t &lo) {
   hi = f2_bf2(x);
-  const float2 h = bf2_f2(hi);
-  lo = f2_bf2(make_float2(x.x - h.x, x.y - h.y));
+  lo = f2_bf2(sub2(x, bf2_f2(hi)));
 }
 
 // The run's tiles one after another, as every warp role walks them.
@@ -164,7 +166,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
   constexpr int HALF = GG::HALF, NST = GG::NST;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[NST], bar_empty[NST];
-  __shared__ int s_j0[NST][NBLK];
+  __shared__ int s_j0[NST][NBLK], s_rho[NST][NBLK];  // a block's first key, and its remainder by G
   __shared__ float red_ml[NCW][PD_HEADS][2];
   __shared__ volatile int abort_flag;
   __shared__ int err_s;
@@ -266,7 +268,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           int page, j0 = -1;
           if (G > 1 && u + (lane >> 2) < w.u1) j0 = paged_block(p, w.s, w.b, kvh, u + (lane >> 2), lane & 3, page);
           if (j0 >= j_local) j0 = -1;  // a local block
-          const int n = j0 >= 0 ? corr_n(j0, G) - ni : 0;
+          const int f = j0 >= 0 ? j0 / G : 0, n = j0 - f - ni, rho = j0 - f * G;
           const unsigned want = __ballot_sync(0xffffffffu, j0 >= 0);
           for (int x = 0; x < 8 && u + x < w.u1; ++x, ++it) {
             if ((it & 1) != par) continue;
@@ -285,6 +287,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (any) {
+              if ((lane >> 2) == x) s_rho[st][lane & 3] = rho;
 #pragma unroll
               for (int blk = 0; blk < NBLK; ++blk)
 #pragma unroll
@@ -319,6 +322,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
         const int L = w.s.L, jw = w.s.jw;
         const int G = p.plain ? 1 : (int)group_size(L, p.w_pre);
         const int j_local = G > 1 ? (int)max(0LL, (long long)L - (long long)p.w0) : 0;
+        // n(j0 + x) - n(j0) = x - floor((rho + x) / G), rho = j0 mod G, x < 16:
+        // by 2^16 / G rounded up where G < 32 (exact for numerators below 2^11), else at most one
+        const uint32_t inv_g = G < 32 ? (65535u + G) / G : 0u;
+        auto turn_in = [&](int rho, int x) { return x - (G < 32 ? (int)(((rho + x) * inv_g) >> 16) : rho + x >= G); };
         // query operand: row = head, channels 16 x + 2 q4 + {0, 1} and + 8
         uint32_t qf[D / 16][2];
         {
@@ -361,8 +368,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
               plain_scores();
             } else {
               // positions by which this lane's two keys (row and row + 8) turn beyond the block's first
-              const int nj = corr_n(j0, G);
-              const int r0 = corr_n(j0 + row, G) - nj, r1 = corr_n(j0 + 8 + row, G) - nj;
+              const int rho = s_rho[st][blk];
+              const int r0 = turn_in(rho, row), r1 = turn_in(rho, row + 8);
               const uint32_t ang = sbase + GG::OFF_ANG + st * GG::ANG + blk * HALF * 8 + q4 * 16;
               const uint32_t tab = sbase + GG::OFF_TAB;
               const uint32_t t0 = tab + r0 * HALF * 8, t1 = tab + r1 * HALF * 8;
@@ -381,17 +388,17 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {  // channels + 8 y
                   const uint32_t at = (x * 16 + y * 8) * 8;
-                  const float4 f = lds_f4(ang + at);
-                  const float2 fc = make_float2(f.x, f.y), fs = make_float2(f.z, f.w);
+                  uint64_t fc, fs;
+                  lds_u64x2(ang + at, fc, fs);
 #pragma unroll
                   for (int nb = 0; nb < 2; ++nb) {
-                    const float4 g = lds_f4((nb ? t1 : t0) + ((at + q4 * 16) ^ (nb ? x1 : x0)));
-                    const float2 gc = make_float2(g.x, g.y), gs = make_float2(g.z, g.w);
-                    const float2 co = fma2(fc, gc, neg2(mul2(fs, gs)));
-                    const float2 si = fma2(fs, gc, mul2(fc, gs));
-                    const float2 a = bf2_f2(ka[2 * nb + y]), b = bf2_f2(kb[2 * nb + y]);
+                    uint64_t gc, gs;
+                    lds_u64x2((nb ? t1 : t0) + ((at + q4 * 16) ^ (nb ? x1 : x0)), gc, gs);
+                    const uint64_t co = sub2(mul2(fc, gc), mul2(fs, gs));
+                    const uint64_t si = fma2(fs, gc, mul2(fc, gs));
+                    const uint64_t a = bf2_f2(ka[2 * nb + y]), b = bf2_f2(kb[2 * nb + y]);
                     split2(fma2(a, co, mul2(b, si)), ah[2 * nb + y], al[2 * nb + y]);
-                    split2(fma2(b, co, neg2(mul2(a, si))), bh[2 * nb + y], bl[2 * nb + y]);
+                    split2(sub2(mul2(b, co), mul2(a, si)), bh[2 * nb + y], bl[2 * nb + y]);
                   }
                 }
 #pragma unroll
@@ -449,9 +456,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             uint32_t ph[2], pl[2];
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb) {
-              const float2 e = make_float2(ex2(sc[nb][0] - mu), ex2(sc[nb][1] - mu));
-              l += e.x + e.y;
-              split2(e, ph[nb], pl[nb]);
+              const float e0 = ex2(sc[nb][0] - mu), e1 = ex2(sc[nb][1] - mu);
+              l += e0 + e1;
+              split2(pack2(e0, e1), ph[nb], pl[nb]);
             }
             // rows 0-7: the weights' high halves, rows 8-15: their low halves
 #pragma unroll
@@ -501,7 +508,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           if (whole) {
             const size_t bh = (size_t)w.b * p.Hq + h0 + g;
             const float r = M != -INFINITY ? 1.f / sum : 0.f;
-            reinterpret_cast<uint32_t *>(p.out)[(bh * D + d) / 2] = f2_bf2(make_float2(acc.x * r, acc.y * r));
+            reinterpret_cast<uint32_t *>(p.out)[(bh * D + d) / 2] = f2_bf2(pack2(acc.x * r, acc.y * r));
             if (p.lse != nullptr && d == 0) p.lse[bh] = M != -INFINITY ? (M + log2f(sum)) * LN2 : -INFINITY;
           } else {
             *reinterpret_cast<float2 *>(p.part_o + (slot * PD_HEADS + g) * D + d) = acc;
