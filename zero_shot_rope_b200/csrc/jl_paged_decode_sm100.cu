@@ -59,7 +59,7 @@ struct Geo {
   static constexpr int OFF_ANG = 2 * NST * KV;
   static constexpr int OFF_TAB = OFF_ANG + NST * ANG;  // turns by 0 .. 15 positions
   static constexpr int OFF_RED = OFF_TAB + PD_BLK * HALF * 8;
-  static constexpr int RS = D + 8;                     // row stride of the merge buffer, padded against bank conflicts
+  static constexpr int RS = D + 4;                     // row stride of the merge buffer: heads 2 apart 8 banks apart
   static constexpr int SMEM = OFF_RED + NCW * PD_HEADS * RS * 4 + 1024;
 };
 static_assert(Geo<128>::SMEM <= 227 * 1024 && Geo<64>::SMEM <= 227 * 1024, "shared memory");
@@ -312,7 +312,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       // ldmatrix addresses within a tile half: K [key][16-byte chunk], and V the same, transposed on the way
       const int lm = lane >> 3, lr = lane & 7;
       const uint32_t k_row = (uint32_t)((blk * PD_BLK + (lm >> 1) * 8 + lr) * 128);
-      const uint32_t v_row = (uint32_t)((blk * PD_BLK + (lm & 1) * 8 + lr) * 128);
+      const uint32_t v_row = (uint32_t)((blk * PD_BLK + (lm >> 1) * 8 + lr) * 128);
       int it = 0;
       bool ok = true;
       while (w.next(p)) {
@@ -337,9 +337,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             qf[x][1] = row < gh ? q[8 * x + 4 + q4] : 0u;
           }
         }
-        float o[D / 8][4], m = -INFINITY, l = 0.f;
+        // outputs, transposed: channels 16 x + row and + 8 of heads 2 q4 + {0, 1}; maximum and sum of head `row`
+        float o[D / 16][4], m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+        for (int x = 0; x < D / 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
 
         for (int u = w.u0; u < w.u1; ++u, ++it) {
           if ((it & 1) != par) continue;
@@ -449,8 +450,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
               const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
               if (grow) m = top;
               l *= f;
+              const float f0 = __shfl_sync(0xffffffffu, f, 8 * q4), f1 = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
 #pragma unroll
-              for (int x = 0; x < D / 8; ++x) o[x][0] *= f, o[x][1] *= f, o[x][2] *= f, o[x][3] *= f;
+              for (int x = 0; x < D / 16; ++x) o[x][0] *= f0, o[x][1] *= f1, o[x][2] *= f0, o[x][3] *= f1;
             }
             const float mu = m == -INFINITY ? 0.f : m;
             uint32_t ph[2], pl[2];
@@ -460,17 +462,17 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
               l += e0 + e1;
               split2(pack2(e0, e1), ph[nb], pl[nb]);
             }
-            // rows 0-7: the weights' high halves, rows 8-15: their low halves
+            // (values^T) (weights^T): a score's lane already holds the weight where the operand wants it
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
               uint32_t vf[4];
-              ldsm4t(vt + (x >> 2) * (PD_TILE * 128) + ((((x & 3) * 2 + (lm >> 1)) ^ lr) << 4), vf);
+              ldsm4t(vt + (x >> 2) * (PD_TILE * 128) + ((((x & 3) * 2 + (lm & 1)) ^ lr) << 4), vf);
               if (part) {  // rows past the length may hold anything, and 0 NaN is NaN
-                vf[0] &= keep[0], vf[2] &= keep[0];
-                vf[1] &= keep[1], vf[3] &= keep[1];
+                vf[0] &= keep[0], vf[1] &= keep[0];
+                vf[2] &= keep[1], vf[3] &= keep[1];
               }
-              mma(o[2 * x], ph[0], pl[0], ph[1], pl[1], vf[0], vf[1]);
-              mma(o[2 * x + 1], ph[0], pl[0], ph[1], pl[1], vf[2], vf[3]);
+              mma(o[x], vf[0], vf[1], vf[2], vf[3], ph[0], ph[1]);
+              mma(o[x], vf[0], vf[1], vf[2], vf[3], pl[0], pl[1]);
             }
           }
           __syncwarp();
@@ -483,9 +485,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
         if (q4 == 0) red_ml[warp][row][0] = m, red_ml[warp][row][1] = l;
         float *red = reinterpret_cast<float *>(gbase + GG::OFF_RED);
 #pragma unroll
-        for (int x = 0; x < D / 8; ++x)
-          *reinterpret_cast<float2 *>(red + (warp * PD_HEADS + row) * GG::RS + 8 * x + 2 * q4) =
-              make_float2(o[x][0] + o[x][2], o[x][1] + o[x][3]);
+        for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            red[(warp * PD_HEADS + 2 * q4 + (e & 1)) * GG::RS + 16 * x + row + 8 * (e >> 1)] = o[x][e];
         asm volatile("bar.sync 1, %0;" ::"n"(NCW * 32) : "memory");
         const bool whole = w.u0 == 0 && w.u1 == w.s.tiles;
         const size_t slot = 2 * (size_t)blockIdx.x + (w.u0 > 0 ? 0 : 1);
