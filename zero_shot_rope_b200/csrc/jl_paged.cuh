@@ -6,6 +6,8 @@
 // of sequence b, its keys cP .. cP + P - 1, is pool page table[b, c].
 #pragma once
 
+#include <utility>
+
 #include "jl_common.cuh"
 
 namespace jl {
@@ -143,21 +145,47 @@ struct PagedRun {
   int b;             // sequence of tile t0
 };
 
-// Computed by the whole block from the lengths on the device, so that a
-// captured step replays with the lengths of the moment.  CTA 0 also leaves the
-// first tile of every sequence in p.tab for the combine.
+__device__ __forceinline__ long long div_up(long long n, int d) {
+  if (n < (1ll << 31)) return (unsigned)(n + d - 1) / (unsigned)d;
+  return (n + d - 1) / d;
+}
+
+// This CTA's run, from the lengths on the device, so that a captured step
+// replays with the lengths of the moment.  CTA 0 also leaves the first tile of
+// every sequence in p.tab for the combine.  Up to 32 sequences: every warp by
+// itself.  More: the whole block, which has to call it together.
 template <int NT>
 __device__ __forceinline__ PagedRun paged_plan(const PagedDecodeArgs &p) {
-  __shared__ long long s_warp[NT / 32], s_run[2];
-  __shared__ int s_b;
+  const unsigned full = 0xffffffffu;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pairs = p.Hkv * p.HB;
-  auto scan = [&](long long x, long long &total) {  // inclusive over the block
+  auto warp_scan = [&](long long x) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      const long long y = __shfl_up_sync(full, x, o);
       if (lane >= o) x += y;
     }
+    return x;
+  };
+  PagedRun r;
+  if (p.B <= 32) {
+    const long long n = lane < p.B ? (long long)paged_seq(p, lane).tiles * pairs : 0;
+    const long long last = warp_scan(n), first = last - n, total = __shfl_sync(full, last, 31);
+    if (blockIdx.x == 0 && warp == 0) {
+      if (lane < p.B) p.tab[lane] = first;
+      if (lane == 0) p.tab[p.B] = total;
+    }
+    const long long chunk = div_up(total, gridDim.x);
+    r.t0 = (long long)blockIdx.x * chunk;
+    r.t1 = r.t0 + chunk < total ? r.t0 + chunk : total;
+    r.b = __ffs(__ballot_sync(full, r.t0 >= first && r.t0 < last)) - 1;
+    r.base = __shfl_sync(full, first, max(r.b, 0));
+    return r;
+  }
+  __shared__ long long s_warp[NT / 32], s_first;
+  __shared__ int s_b;
+  auto scan = [&](long long x, long long &total) {  // inclusive over the block
+    x = warp_scan(x);
     __syncthreads();
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
@@ -173,8 +201,7 @@ __device__ __forceinline__ PagedRun paged_plan(const PagedDecodeArgs &p) {
   long long mine = 0, total;
   for (int b = tid; b < p.B; b += NT) mine += (long long)paged_seq(p, b).tiles * pairs;
   scan(mine, total);
-  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
-  PagedRun r;
+  const long long chunk = div_up(total, gridDim.x);
   r.t0 = (long long)blockIdx.x * chunk;
   r.t1 = r.t0 + chunk < total ? r.t0 + chunk : total;
   if (tid == 0) s_b = -1;
@@ -189,7 +216,7 @@ __device__ __forceinline__ PagedRun paged_plan(const PagedDecodeArgs &p) {
       if (blockIdx.x == 0) p.tab[b] = first;
       if (r.t0 >= first && r.t0 < first + n) {
         s_b = b;
-        s_run[0] = first;
+        s_first = first;
       }
     }
     carry += sum;
@@ -198,9 +225,60 @@ __device__ __forceinline__ PagedRun paged_plan(const PagedDecodeArgs &p) {
   if (blockIdx.x == 0 && tid == 0) p.tab[p.B] = carry;
   __syncthreads();
   r.b = s_b;
-  r.base = s_run[0];
-  if (r.t0 >= r.t1) r.b = -1;
+  r.base = s_first;
   return r;
+}
+
+// The run's tiles piece by piece (a piece: tiles u0 .. u1 - 1 of one (kv head,
+// head block) of sequence b), as every warp walks them.
+struct PagedWalk {
+  long long base, t, t1;
+  int b, pairs;
+  PagedSeq s;
+  int pair, u0, u1;
+  __device__ __forceinline__ PagedWalk(const PagedDecodeArgs &p, const PagedRun &r)
+      : base(r.base), t(r.t0), t1(r.b >= 0 ? r.t1 : r.t0), b(r.b), pairs(p.Hkv * p.HB) {}
+  __device__ __forceinline__ bool next(const PagedDecodeArgs &p) {
+    while (t < t1) {
+      s = paged_seq(p, b);
+      const long long n = (long long)s.tiles * pairs;
+      if (t >= base + n) {
+        base += n;
+        ++b;
+        continue;
+      }
+      const long long at = t - base;
+      pair = at < (1ll << 31) ? (int)((unsigned)at / (unsigned)s.tiles) : (int)(at / s.tiles);
+      u0 = (int)(at - (long long)pair * s.tiles);
+      u1 = (int)(t1 - t < s.tiles - u0 ? u0 + (t1 - t) : s.tiles);
+      t += u1 - u0;
+      return true;
+    }
+    return false;
+  }
+};
+
+// ------------------------------------------------------- dependent launches
+// The paged-cache kernels are launched so that their set-up overlaps the end of
+// the kernel before them (programmatic dependent launch): each waits for all of
+// that kernel's work before it touches global memory, and lets the next one's
+// blocks come as soon as its own are placed.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_come() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A &&...args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 // The tensor-core kernel (bf16): the partial results only; paged_decode_tc_ctas() runs.

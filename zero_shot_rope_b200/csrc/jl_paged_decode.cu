@@ -45,11 +45,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
   constexpr int PPL = D / 64, HALF = D / 2, KW = 8;
   __shared__ float red_ml[NW][GP][2];
   __shared__ float red_o[NW][GP][D];
+  let_next_kernel_come();
+  wait_for_kernel_before();
   const PagedRun run = paged_plan<NT>(p);
   if (threadIdx.x == 0) p.cta_err[blockIdx.x] = 0;  // this kernel has no waits that could run out
-  if (run.b < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int pairs = p.Hkv * p.HB;
   const float scale = rsqrtf((float)D) * LOG2E_F;
   double w[PPL];
   float c1[PPL], s1[PPL];  // rotation by one position
@@ -59,18 +59,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
     angle_cs(1, w[e], c1[e], s1[e]);
   }
 
-  int b = run.b;
-  long long base = run.base, t = run.t0;
-  while (t < run.t1) {
-    const PagedSeq s = paged_seq(p, b);
-    const long long n = (long long)s.tiles * pairs;
-    if (t >= base + n) {
-      base += n;
-      ++b;
-      continue;
-    }
-    const int pair = (int)((t - base) / s.tiles), u0 = (int)((t - base) % s.tiles);
-    const int u1 = (int)(run.t1 - t < s.tiles - u0 ? u0 + (run.t1 - t) : s.tiles);
+  PagedWalk walk(p, run);
+  while (walk.next(p)) {
+    const PagedSeq &s = walk.s;
+    const int b = walk.b, pair = walk.pair, u0 = walk.u0, u1 = walk.u1;
     const int kvh = pair / p.HB, hb = pair % p.HB;
     const int gh = min(PD_HEADS, p.GS - hb * PD_HEADS);
     const int h0 = kvh * p.GS + hb * PD_HEADS;  // first query head
@@ -204,93 +196,145 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
         }
       }
     }
-    t += u1 - u0;
   }
 }
 
 // Joins the runs' partial results of one (kv head, head block) of a sequence,
 // or writes zeros and -inf where the sequence has no key.  Pairs that one run
-// covered whole were finished there.
+// covered whole were finished there.  Two dependent reads of global memory: the
+// plan's table, then all maxima, sums and partial outputs at once (a thread
+// reads its outputs before the weights they will get are known).
 template <typename T, int D>
 __global__ void __launch_bounds__(NT)
 paged_combine_kernel(const __grid_constant__ PagedDecodeArgs p, int ctas) {
+  constexpr int VPT = PD_HEADS * D / 4 / NT;  // float4s of the pair's outputs per thread, 1 (or a half: D = 64)
+  constexpr int XG = VPT > 0 ? 1 : 2;         // groups of threads that share the runs
+  constexpr int AHEAD = 8;                    // partial outputs a thread reads ahead
   __shared__ float w_s[PD_MAX_CTAS][PD_HEADS];
   __shared__ float M_s[PD_HEADS], L_s[PD_HEADS];
+  __shared__ float4 acc_s[XG > 1 ? NT / 2 : 1];
   const int b = blockIdx.y, pair = blockIdx.x, pairs = p.Hkv * p.HB;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kvh = pair / p.HB, hb = pair % p.HB;
   const int gh = min(PD_HEADS, p.GS - hb * PD_HEADS);
   const int h0 = kvh * p.GS + hb * PD_HEADS;
-  if (blockIdx.x == 0 && b == 0 && threadIdx.x < 32) {  // fold the CTAs' error words
-    int e = 0;
-    for (int x = threadIdx.x; x < ctas; x += 32) e |= p.cta_err[x];
-    e = __reduce_or_sync(0xffffffffu, e);
-    if (threadIdx.x == 0) *p.err = e;
-  }
-  const long long first = p.tab[b], tiles = (p.tab[b + 1] - first) / pairs;
-  const long long total = p.tab[p.B];
   const size_t bh0 = (size_t)b * p.Hq + h0;
-  if (tiles == 0) {
-    for (int idx = threadIdx.x; idx < gh * D; idx += NT) ((T *)p.out)[bh0 * D + idx] = from_f<T>(0.f);
-    if (p.lse != nullptr && threadIdx.x < gh) p.lse[bh0 + threadIdx.x] = -INFINITY;
+  let_next_kernel_come();
+  wait_for_kernel_before();
+  const long long first = p.tab[b], next = p.tab[b + 1], total = p.tab[p.B];
+  if (pair == 0 && b == 0 && tid < 32) {  // fold the CTAs' error words
+    int e = 0;
+    for (int x = tid; x < ctas; x += 32) e |= p.cta_err[x];
+    e = __reduce_or_sync(0xffffffffu, e);
+    if (tid == 0) *p.err = e;
+  }
+  if (next == first) {
+    for (int idx = tid; idx < gh * D; idx += NT) ((T *)p.out)[bh0 * D + idx] = from_f<T>(0.f);
+    if (p.lse != nullptr && tid < gh) p.lse[bh0 + tid] = -INFINITY;
     return;
   }
-  const long long chunk = (total + ctas - 1) / ctas;
+  const long long tiles = div_up(next - first, pairs), chunk = div_up(total, ctas);
   const long long p0 = first + pair * tiles, p1 = p0 + tiles;
-  const int c0 = (int)(p0 / chunk), c1 = (int)((p1 - 1) / chunk);
+  auto cta_of = [&](long long t) {
+    return total < (1ll << 31) ? (int)((unsigned)t / (unsigned)chunk) : (int)(t / chunk);
+  };
+  const int c0 = cta_of(p0), c1 = cta_of(p1 - 1);
   if (c0 == c1) return;  // covered whole
   const int ns = c1 - c0 + 1;
-  // the pair's first run holds it in its second slot, unless it begins there
+  // the pair's first run holds it in its second slot: the run has other pairs before it, or none
   auto slot = [&](int x) { return 2 * (size_t)(c0 + x) + (x == 0 ? 1 : 0); };
-  for (int idx = threadIdx.x; idx < ns * PD_HEADS; idx += NT) {
-    const int x = idx / PD_HEADS, g = idx % PD_HEADS;
-    w_s[x][g] = g < gh ? p.part_ml[(slot(x) * PD_HEADS + g) * 2] : -INFINITY;
-  }
-  __syncthreads();
-  if (threadIdx.x < PD_HEADS) {
-    const int g = threadIdx.x;
+  // this thread's float4 of the outputs (head vg), over runs xg, xg + XG, ...
+  const int v = tid % (PD_HEADS * D / 4), xg = tid / (PD_HEADS * D / 4);
+  const int vg = v / (D / 4);
+  const float4 *part = reinterpret_cast<const float4 *>(p.part_o) + v;
+  const bool mine = vg < gh;
+  float4 buf[AHEAD];
+  if (mine)
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a)
+      if (xg + a * XG < ns) buf[a] = part[slot(xg + a * XG) * (PD_HEADS * D / 4)];
+  // warp g: maximum, weights and sum of head g
+  {
+    const int g = warp;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + g;
+    float2 y[3];
     float M = -INFINITY;
-    for (int x = 0; x < ns; ++x) M = max_nan(M, w_s[x][g]);
-    M_s[g] = M;
-  }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < ns * PD_HEADS; idx += NT) {
-    const int x = idx / PD_HEADS, g = idx % PD_HEADS;
-    w_s[x][g] = M_s[g] == -INFINITY ? 0.f : exp2f(w_s[x][g] - M_s[g]);
-  }
-  __syncthreads();
-  if (threadIdx.x < PD_HEADS) {
-    const int g = threadIdx.x;
+    for (int x0 = 0; x0 < ns; x0 += 96)
+#pragma unroll
+      for (int a = 0; a < 3; ++a) {
+        const int x = x0 + 32 * a + lane;
+        y[a] = g < gh && x < ns ? ml[slot(x) * PD_HEADS] : make_float2(-INFINITY, 0.f);
+        M = max_nan(M, y[a].x);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
     float L = 0.f;
-    if (g < gh)
-      for (int x = 0; x < ns; ++x) L = fmaf(w_s[x][g], p.part_ml[(slot(x) * PD_HEADS + g) * 2 + 1], L);
-    L_s[g] = L;
-    if (g < gh && p.lse != nullptr) p.lse[bh0 + g] = M_s[g] == -INFINITY ? -INFINITY : (M_s[g] + log2f(L)) * LN2;
+    for (int x0 = 0; x0 < ns; x0 += 96)
+#pragma unroll
+      for (int a = 0; a < 3; ++a) {
+        const int x = x0 + 32 * a + lane;
+        if (ns > 96) y[a] = g < gh && x < ns ? ml[slot(x) * PD_HEADS] : make_float2(-INFINITY, 0.f);
+        const float f = M == -INFINITY ? 0.f : exp2f(y[a].x - M);
+        if (x < ns) w_s[x][g] = f;
+        L = fmaf(f, y[a].y, L);
+      }
+    L = warp_sum(L);
+    if (lane == 0) {
+      M_s[g] = M;
+      L_s[g] = L;
+      if (g < gh && p.lse != nullptr) p.lse[bh0 + g] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * LN2;
+    }
   }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < gh * D; idx += NT) {
-    const int g = idx / D, d = idx % D;
-    float acc = 0.f;
-#pragma unroll 4
-    for (int x = 0; x < ns; ++x) acc = fmaf(w_s[x][g], p.part_o[(slot(x) * PD_HEADS + g) * D + d], acc);
-    ((T *)p.out)[bh0 * D + idx] = from_f<T>(M_s[g] == -INFINITY ? 0.f : acc / L_s[g]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mine)
+    for (int x0 = xg; x0 < ns; x0 += AHEAD * XG) {
+      if (x0 != xg)
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+          if (x0 + a * XG < ns) buf[a] = part[slot(x0 + a * XG) * (PD_HEADS * D / 4)];
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a)
+        if (x0 + a * XG < ns) {
+          const float f = w_s[x0 + a * XG][vg];
+          acc.x = fmaf(f, buf[a].x, acc.x), acc.y = fmaf(f, buf[a].y, acc.y);
+          acc.z = fmaf(f, buf[a].z, acc.z), acc.w = fmaf(f, buf[a].w, acc.w);
+        }
+    }
+  if constexpr (XG > 1) {
+    if (xg == 1) acc_s[v] = acc;
+    __syncthreads();
+    if (xg == 1) return;
+    const float4 y = acc_s[v];
+    acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+  }
+  if (mine) {
+    const float r = M_s[vg] == -INFINITY ? 0.f : 1.f / L_s[vg];
+    T *to = (T *)p.out + (bh0 + vg) * D + (v % (D / 4)) * 4;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4 *>(to) = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * r, acc.y * r), y = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+      *reinterpret_cast<uint2 *>(to) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    }
   }
 }
 
 template <typename T, int D>
 cudaError_t combine(const PagedDecodeArgs &a, int ctas, cudaStream_t st) {
-  paged_combine_kernel<T, D><<<dim3(a.Hkv * a.HB, a.B), NT, 0, st>>>(a, ctas);
-  return cudaGetLastError();
+  return launch_overlapped(paged_combine_kernel<T, D>, dim3(a.Hkv * a.HB, a.B), NT, 0, st, a, ctas);
 }
 
 template <int D>
 cudaError_t launch_fp32(const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
   constexpr int ctas = 296;
   const int gp = a.GS > PD_HEADS ? PD_HEADS : a.GS;
-  if (gp == 1) paged_decode_kernel<float, D, 1><<<ctas, NT, 0, st>>>(a, inv);
-  else if (gp == 2) paged_decode_kernel<float, D, 2><<<ctas, NT, 0, st>>>(a, inv);
-  else if (gp <= 4) paged_decode_kernel<float, D, 4><<<ctas, NT, 0, st>>>(a, inv);
-  else paged_decode_kernel<float, D, 8><<<ctas, NT, 0, st>>>(a, inv);
-  const cudaError_t e = cudaGetLastError();
+  const auto kernel = gp == 1   ? paged_decode_kernel<float, D, 1>
+                      : gp == 2 ? paged_decode_kernel<float, D, 2>
+                      : gp <= 4 ? paged_decode_kernel<float, D, 4>
+                                : paged_decode_kernel<float, D, 8>;
+  const cudaError_t e = launch_overlapped(kernel, ctas, NT, 0, st, a, inv);
   return e != cudaSuccess ? e : combine<float, D>(a, ctas, st);
 }
 

@@ -64,12 +64,12 @@ struct Geo {
 };
 static_assert(Geo<128>::SMEM <= 227 * 1024 && Geo<64>::SMEM <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ void tma_load4(const CUtensorMap *map, uint64_t *bar, uint32_t dst, int c0, int c1, int c2,
-                                          int c3) {
+__device__ __forceinline__ void tma_load5(const CUtensorMap *map, uint64_t *bar, uint32_t dst, int c0, int c1, int c2,
+                                          int c3, int c4) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(map), "r"(su32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(map), "r"(su32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -131,33 +131,6 @@ __device__ __forceinline__ void split2(uint64_t x, uint32_t &hi, uint32_t &lo) {
   lo = f2_bf2(sub2(x, bf2_f2(hi)));
 }
 
-// The run's tiles one after another, as every warp role walks them.
-struct Walk {
-  long long base, t, t1;
-  int b, pairs;
-  PagedSeq s;
-  int pair, u0, u1;  // current piece: tiles u0 .. u1 - 1 of a pair
-  __device__ __forceinline__ Walk(const PagedDecodeArgs &p, const PagedRun &r)
-      : base(r.base), t(r.t0), t1(r.t1), b(r.b), pairs(p.Hkv * p.HB) {}
-  __device__ __forceinline__ bool next(const PagedDecodeArgs &p) {
-    while (t < t1) {
-      s = paged_seq(p, b);
-      const long long n = (long long)s.tiles * pairs;
-      if (t >= base + n) {
-        base += n;
-        ++b;
-        continue;
-      }
-      pair = (int)((t - base) / s.tiles);
-      u0 = (int)((t - base) % s.tiles);
-      u1 = (int)(t1 - t < s.tiles - u0 ? u0 + (t1 - t) : s.tiles);
-      t += u1 - u0;
-      return true;
-    }
-    return false;
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
 paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
@@ -194,15 +167,17 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
     to[k & 1] = c;
     to[2 + (k & 1)] = s;
   }
+  let_next_kernel_come();
+  wait_for_kernel_before();
   const PagedRun run = paged_plan<THREADS>(p);
   __syncthreads();
 
-  Walk w(p, run);
+  PagedWalk w(p, run);
   if (run.b >= 0) {
     if (warp == WARP_LOAD) {
       // ======================= producer =======================
       const int rows = min(1 << p.page_log2, PD_TILE);  // rows of a box
-      const int runs = PD_TILE / rows;                  // boxes of K (and V) per 64 channels of a tile
+      const int runs = PD_TILE / rows;                  // boxes of K (and of V) of a tile
       const int per = rows / PD_BLK;                    // blocks of a box
       int it = 0;
       bool ok = true;
@@ -237,12 +212,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             const int bp = __shfl_sync(0xffffffffu, page, src), bj = __shfl_sync(0xffffffffu, j0, src);
             if (lane < runs && bj >= 0) {
               const int slot = (bj & ((1 << p.page_log2) - 1)) & ~(rows - 1);
-              const uint32_t to = sbase + st * GG::KV + lane * rows * 128;
-#pragma unroll
-              for (int h = 0; h < GG::NH; ++h) {
-                tma_load4(&mK, &bar_full[st], to + GG::OFF_K + h * (PD_TILE * 128), 64 * h, kvh, slot, bp);
-                tma_load4(&mV, &bar_full[st], to + GG::OFF_V + h * (PD_TILE * 128), 64 * h, kvh, slot, bp);
-              }
+              const uint32_t to = sbase + st * GG::KV + lane * rows * D * 2;
+              tma_load5(&mK, &bar_full[st], to + GG::OFF_K, 0, kvh, slot, bp, 0);
+              tma_load5(&mV, &bar_full[st], to + GG::OFF_V, 0, kvh, slot, bp, 0);
             }
             __syncwarp();
           }
@@ -311,8 +283,11 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       const float scale = rsqrtf((float)D) * 1.4426950408889634f;
       // ldmatrix addresses within a tile half: K [key][16-byte chunk], and V the same, transposed on the way
       const int lm = lane >> 3, lr = lane & 7;
-      const uint32_t k_row = (uint32_t)((blk * PD_BLK + (lm >> 1) * 8 + lr) * 128);
-      const uint32_t v_row = (uint32_t)((blk * PD_BLK + (lm >> 1) * 8 + lr) * 128);
+      // (a box of `rows` keys: 64 channels of each key in turn, then the other 64)
+      const int rows = min(1 << p.page_log2, PD_TILE);
+      const uint32_t half_b = D == 128 ? rows * 128 : 0;
+      const uint32_t kv_row = (uint32_t)(blk * PD_BLK / rows * rows * D * 2 +
+                                         (blk * PD_BLK % rows + (lm >> 1) * 8 + lr) * 128);
       int it = 0;
       bool ok = true;
       while (w.next(p)) {
@@ -350,8 +325,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           if (!ok) continue;  // the run is walked to its end, so that the merges' barriers are met
           const int j0 = s_j0[st][blk];
           if (j0 >= 0) {
-            const uint32_t kt = sbase + GG::OFF_K + st * GG::KV + k_row;
-            const uint32_t vt = sbase + GG::OFF_V + st * GG::KV + v_row;
+            const uint32_t kt = sbase + GG::OFF_K + st * GG::KV + kv_row;
+            const uint32_t vt = sbase + GG::OFF_V + st * GG::KV + kv_row;
             // scores of keys 8 nb + 2 q4 + {0, 1} for head `row` in c[nb][0..1]
             float sc[2][2];
             auto plain_scores = [&]() {
@@ -359,7 +334,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
 #pragma unroll
               for (int x = 0; x < D / 16; ++x) {
                 uint32_t kf[4];
-                ldsm4(kt + (x >> 2) * (PD_TILE * 128) + ((((x & 3) * 2 + (lm & 1)) ^ lr) << 4), kf);
+                ldsm4(kt + (x >> 2) * half_b + ((((x & 3) * 2 + (lm & 1)) ^ lr) << 4), kf);
                 mma(c[0], qf[x][0], 0u, qf[x][1], 0u, kf[0], kf[1]);
                 mma(c[1], qf[x][0], 0u, qf[x][1], 0u, kf[2], kf[3]);
               }
@@ -382,7 +357,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
                 uint32_t ka[4], kb[4];
                 ldsm4(kt + (((x * 2 + (lm & 1)) ^ lr) << 4), ka);
                 if constexpr (D == 128)
-                  ldsm4(kt + PD_TILE * 128 + (((x * 2 + (lm & 1)) ^ lr) << 4), kb);
+                  ldsm4(kt + half_b + (((x * 2 + (lm & 1)) ^ lr) << 4), kb);
                 else
                   ldsm4(kt + (((4 + x * 2 + (lm & 1)) ^ lr) << 4), kb);
                 uint32_t ah[4], al[4], bh[4], bl[4];
@@ -466,7 +441,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
               uint32_t vf[4];
-              ldsm4t(vt + (x >> 2) * (PD_TILE * 128) + ((((x & 3) * 2 + (lm & 1)) ^ lr) << 4), vf);
+              ldsm4t(vt + (x >> 2) * half_b + ((((x & 3) * 2 + (lm & 1)) ^ lr) << 4), vf);
               if (part) {  // rows past the length may hold anything, and 0 NaN is NaN
                 vf[0] &= keep[0], vf[1] &= keep[0];
                 vf[2] &= keep[1], vf[3] &= keep[1];
@@ -530,15 +505,15 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
 }
 
 static bool make_pool_map(CUtensorMap *m, const void *base, const PagedDecodeArgs &a, int D) {
-  // a pool viewed as (d, head, slot, page)
+  // a pool viewed as (channel of 64, head, slot, page, 64 channels)
   static EncodeTiledFn enc = get_encode_tiled();
   if (enc == nullptr) return false;
   const int P = 1 << a.page_log2;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hkv, (cuuint64_t)P, (cuuint64_t)a.n_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hkv * D * 2, (cuuint64_t)a.page_stride * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)(P < PD_TILE ? P : PD_TILE), 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+  const cuuint64_t dims[5] = {64, (cuuint64_t)a.Hkv, (cuuint64_t)P, (cuuint64_t)a.n_pages, (cuuint64_t)D / 64};
+  const cuuint64_t strides[4] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hkv * D * 2, (cuuint64_t)a.page_stride * 2, 128};
+  const cuuint32_t box[5] = {64, 1, (cuuint32_t)(P < PD_TILE ? P : PD_TILE), 1, (cuuint32_t)D / 64};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -555,14 +530,15 @@ cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const TurnFr
     e = cudaFuncSetAttribute(pgt::paged_decode_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              pgt::Geo<128>::SMEM);
     if (e != cudaSuccess) return e;
-    pgt::paged_decode_tc_kernel<128><<<pgt::CTAS, pgt::THREADS, pgt::Geo<128>::SMEM, st>>>(mK, mV, a, turn);
+    return launch_overlapped(pgt::paged_decode_tc_kernel<128>, pgt::CTAS, pgt::THREADS, pgt::Geo<128>::SMEM, st, mK, mV, a,
+                             turn);
   } else {
     e = cudaFuncSetAttribute(pgt::paged_decode_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              pgt::Geo<64>::SMEM);
     if (e != cudaSuccess) return e;
-    pgt::paged_decode_tc_kernel<64><<<pgt::CTAS, pgt::THREADS, pgt::Geo<64>::SMEM, st>>>(mK, mV, a, turn);
+    return launch_overlapped(pgt::paged_decode_tc_kernel<64>, pgt::CTAS, pgt::THREADS, pgt::Geo<64>::SMEM, st, mK, mV, a,
+                             turn);
   }
-  return cudaGetLastError();
 }
 
 // Test hook: the limit of the bounded waits of this file's kernels.
