@@ -310,6 +310,8 @@ SELECT = [
     ((9000, 2000), 32, 17, 1, 128, F32, 9999, 100, 11, 0, 0),
     ((20000,), 16, 4, 4, 64, F32, 3000, 0, 600, 10, 20),
     ((8191,), 256, 8, 1, 128, BF, 512, 9000, 3, 0, 1),
+    ((150001, 40000), 16, 4, 2, 64, BF, 30000, 1000, 40, 1, 1),  # more pages than a CTA keeps in registers
+    ((33000, 2000), 16, 2, 1, 64, F32, 5000, 100, 2050, 1, 1),   # a list longer than a short sequence's pages
 ]
 
 

@@ -72,6 +72,25 @@ jl::TurnFreq make_turn_freq(const jl::InvFreq &inv) {
   return f;
 }
 
+// Both for the last (head_dim, theta) of the calling thread: a model has one,
+// and 64 powers take as long as a launch.
+struct Freqs {
+  int D = 0;
+  double theta = 0.0;
+  jl::InvFreq inv;
+  jl::TurnFreq turn;
+};
+const Freqs &freqs_of(int D, double theta) {
+  static thread_local Freqs f;
+  if (f.D != D || f.theta != theta) {
+    f.inv = make_inv_freq(D, theta);
+    f.turn = make_turn_freq(f.inv);
+    f.D = D;
+    f.theta = theta;
+  }
+  return f;
+}
+
 jl_status check_heads(int32_t Hq, int32_t Hkv, int32_t D) {
   if (Hq <= 0 || Hkv <= 0) return fail(JL_ERR_INVALID_ARG, "head counts must be positive (Hq=%d, Hkv=%d)", Hq, Hkv);
   if (Hq % Hkv != 0) return fail(JL_ERR_INVALID_ARG, "n_q_heads (%d) is not a multiple of n_kv_heads (%d)", Hq, Hkv);
@@ -361,15 +380,15 @@ jl_status jl_paged_append(const void *k, const void *v, void *k_pages, void *v_p
   a.Hkv = n_kv_heads;
   a.GS = n_q_heads / n_kv_heads;
   a.page_stride = page_stride;
-  const jl::InvFreq inv = make_inv_freq(head_dim, rotate ? rope_theta : 1.0);
-  const cudaError_t e = jl::launch_paged_append(dtype == JL_BF16, head_dim, rotate, a, inv, batch, (cudaStream_t)stream);
+  const cudaError_t e = jl::launch_paged_append(dtype == JL_BF16, head_dim, rotate, a,
+                                                freqs_of(head_dim, rotate ? rope_theta : 1.0).inv, batch, (cudaStream_t)stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "paged append launch");
 }
 
 size_t jl_bifocal_select_pages_workspace_size(int32_t batch, int32_t n_kv_heads, int32_t max_pages, int32_t n_select) {
   if (batch <= 0 || n_kv_heads <= 0 || max_pages <= 0 || n_select <= 0 || max_pages <= n_select) return 0;
   const size_t n = (size_t)batch * n_kv_heads * max_pages;
-  return 3 * align256(n * sizeof(float)) + align256(n * sizeof(double));
+  return 4 * align256(n * sizeof(float)) + align256(n * sizeof(double));
 }
 
 jl_status jl_bifocal_select_pages(const void *q, const void *page_summary, const int32_t *block_table,
@@ -419,10 +438,11 @@ jl_status jl_bifocal_select_pages(const void *q, const void *page_summary, const
   a.list = page_list;
   a.score = (float *)workspace;
   a.mx = (float *)((char *)workspace + align256(n * sizeof(float)));
-  a.amb = (int32_t *)((char *)workspace + 2 * align256(n * sizeof(float)));
-  a.fine = (double *)((char *)workspace + 3 * align256(n * sizeof(float)));
-  const jl::InvFreq inv = make_inv_freq(head_dim, rope_theta);
-  const cudaError_t e = jl::launch_paged_select(dtype == JL_BF16, head_dim, a, inv, (cudaStream_t)stream);
+  a.mark = (float *)((char *)workspace + 2 * align256(n * sizeof(float)));
+  a.amb = (int32_t *)((char *)workspace + 3 * align256(n * sizeof(float)));
+  a.fine = (double *)((char *)workspace + 4 * align256(n * sizeof(float)));
+  const Freqs &f = freqs_of(head_dim, rope_theta);
+  const cudaError_t e = jl::launch_paged_select(dtype == JL_BF16, head_dim, a, f.inv, f.turn, (cudaStream_t)stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "page selection launch");
 }
 
@@ -492,8 +512,8 @@ jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void
   a.tab = (long long *)((char *)a.part_ml + align256(rows * 2 * sizeof(float)));
   a.out = out;
   a.lse = lse;
-  const jl::InvFreq inv = make_inv_freq(head_dim, rope_theta);
-  const cudaError_t e = jl::launch_paged_decode(dtype == JL_BF16, head_dim, a, inv, make_turn_freq(inv), (cudaStream_t)stream);
+  const Freqs &f = freqs_of(head_dim, rope_theta);
+  const cudaError_t e = jl::launch_paged_decode(dtype == JL_BF16, head_dim, a, f.inv, f.turn, (cudaStream_t)stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "paged decode launch");
 }
 

@@ -309,10 +309,15 @@ struct PagedSelectArgs {
   long long w_pre;
   int w0, plain;
   int32_t *list;
-  float *score, *mx;  // [B, Hkv, max_pages]
-  double *fine;       // [B, Hkv, max_pages]
-  int32_t *amb;       // [B, Hkv, max_pages]
+  // [B, Hkv, max_pages] each: a page's fp32 score; the largest |min|, |max| of a
+  // group of mx_pages pages; 1 for a chosen page; the undecided pages and their
+  // scores in 64 bits
+  float *score, *mx, *mark;
+  int mx_pages;
+  int32_t *amb;
+  double *fine;
 };
-cudaError_t launch_paged_select(bool bf16, int D, const PagedSelectArgs &a, const InvFreq &inv, cudaStream_t st);
+cudaError_t launch_paged_select(bool bf16, int D, const PagedSelectArgs &a, const InvFreq &inv, const TurnFreq &turn,
+                                cudaStream_t st);
 
 }  // namespace jl

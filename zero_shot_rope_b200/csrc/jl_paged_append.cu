@@ -62,6 +62,8 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
   __shared__ float2 cs[ROT ? CHUNK : 1][HALF];
   __shared__ float red[2][NT / 32][D];
   const int b = blockIdx.z, kvh = blockIdx.y;
+  let_next_kernel_come();
+  wait_for_kernel_before();
   const int c0 = a.cu[b], n = a.cu[b + 1] - c0, L = a.seqlens[b];
   // outside the contract: the sequence is left alone
   if (c0 < 0 || n <= 0 || n > a.max_new || n > L || c0 > a.T - n) return;
@@ -184,9 +186,8 @@ template <typename T, int D>
 cudaError_t launch(bool rotate, const PagedAppendArgs &a, const InvFreq &inv, int batch, cudaStream_t st) {
   const int P = 1 << a.page_log2;
   const dim3 grid((unsigned)(((long long)a.max_new + 2 * P - 2) / P), a.Hkv, batch);
-  if (rotate) paged_append_kernel<T, D, true><<<grid, NT, 0, st>>>(a, inv);
-  else paged_append_kernel<T, D, false><<<grid, NT, 0, st>>>(a, inv);
-  return cudaGetLastError();
+  const auto kernel = rotate ? paged_append_kernel<T, D, true> : paged_append_kernel<T, D, false>;
+  return launch_overlapped(kernel, grid, NT, 0, st, a, inv);
 }
 
 }  // namespace pga

@@ -265,108 +265,112 @@ def jl_bifocal_decode_noalloc_error(stream=None) -> int:
 # The paged calls also check shapes, types, strides and devices here (the C
 # ABI sees pointers only), run on the device of their tensors whichever is
 # current, and allocate what the caller did not pass on the stream they run on.
+# A generation step makes three of them per layer, so what they do on the host
+# is kept short: each tensor is checked by one expression, and only a misfit is
+# looked at in detail.
 
-class _On:
-    """Makes ``device`` and ``stream`` current, where they are not already."""
-
-    __slots__ = ("ctx", "raw")
-
-    def __init__(self, device, stream):
-        self.ctx = None
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device (got {device})")
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, tensors on {device}")
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _tensor(name, t, shape, dtype, device):
-    """Raise unless t is a contiguous tensor of this shape (-1: any extent),
-    type and device."""
-    if tuple(t.shape) != shape and (t.dim() != len(shape) or
-                                    any(w != -1 and w != n for w, n in zip(shape, t.shape))):
+def _fits(t, shape, dtype, index):
+    return t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+
+
+def _misfit(name, t, shape, dtype, device):
+    """Raise for a tensor that is not a contiguous one of this shape, type and
+    device."""
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)} (got {list(t.shape)})")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _pools(k_pages, v_pages, n_kv_heads, head_dim, dtype, device):
+def _tensor(name, t, shape, dtype, like):
+    if not _fits(t, shape, dtype, like.get_device()):
+        _misfit(name, t, shape, dtype, like.device)
+
+
+def _pools(k_pages, v_pages, n_kv_heads, head_dim, like):
     """(page size, pages, stride between pages) of the two pools."""
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[2:] != (n_kv_heads, head_dim):
+    shape, dtype, index = k_pages.shape, like.dtype, like.get_device()
+    if len(shape) != 4 or shape != v_pages.shape or shape[2] != n_kv_heads or shape[3] != head_dim:
         raise ValueError(f"k_pages and v_pages must both be [n_pages, page_size, {n_kv_heads}, {head_dim}] "
                          f"(got {list(k_pages.shape)}, {list(v_pages.shape)})")
+    n, page = shape[0], shape[1]
+    whole = page * n_kv_heads * head_dim
+    if n > 0 and _fits(k_pages, shape, dtype, index) and _fits(v_pages, shape, dtype, index):
+        return page, n, whole
     if k_pages.dtype != dtype or v_pages.dtype != dtype:
         raise TypeError(f"k_pages and v_pages must be {dtype} (got {k_pages.dtype}, {v_pages.dtype})")
-    if k_pages.device != device or v_pages.device != device:
-        raise ValueError(f"k_pages and v_pages must be on {device}")
-    n, page = k_pages.shape[0], k_pages.shape[1]
+    if k_pages.device != like.device or v_pages.device != like.device:
+        raise ValueError(f"k_pages and v_pages must be on {like.device}")
     if n == 0:
         raise ValueError("the pools have no page")
-    if k_pages.is_contiguous() and v_pages.is_contiguous():
-        return page, n, page * n_kv_heads * head_dim
     if not (k_pages[0].is_contiguous() and v_pages[0].is_contiguous()):
         raise ValueError("each page of k_pages and v_pages must be contiguous")
     if n == 1:
-        return page, n, page * n_kv_heads * head_dim
+        return page, n, whole
     if k_pages.stride(0) != v_pages.stride(0):
         raise ValueError("k_pages and v_pages must have the same stride between pages")
     return page, n, k_pages.stride(0)
 
 
-def _table(block_table, batch, device):
+def _table(block_table, batch, like):
     """(pages per sequence, row stride) of the block table."""
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError(f"block_table must have shape [{batch}, max_pages] (got {list(block_table.shape)})")
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != batch:
+        raise ValueError(f"block_table must have shape [{batch}, max_pages] (got {list(shape)})")
+    cols = shape[1]
+    if _fits(block_table, shape, torch.int32, like.get_device()):
+        return cols, cols
     if block_table.dtype != torch.int32:
         raise TypeError(f"block_table must be torch.int32 (got {block_table.dtype})")
-    if block_table.device != device:
-        raise ValueError(f"block_table is on {block_table.device}, expected {device}")
-    cols = block_table.shape[1]
+    if block_table.device != like.device:
+        raise ValueError(f"block_table is on {block_table.device}, expected {like.device}")
     if cols > 1 and block_table.stride(1) != 1:
         raise ValueError("block_table's rows must be contiguous")
     return cols, (block_table.stride(0) if batch > 1 else cols)
-
-
-def _given(name, t, shape, dtype, device):
-    """t if it is fit to be written, a new tensor if there is none."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _tensor(name, t, shape, dtype, device)
-    return t
-
-
-def _scratch(workspace, nbytes, device):
-    """(tensor, pointer, bytes) of the workspace; the tensor keeps it alive."""
-    if nbytes == 0:
-        return None, None, 0
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        return workspace, workspace.data_ptr(), nbytes
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _heads3(name, t):
     if t.dim() != 3:
         raise ValueError(f"{name} must have three dimensions (got {list(t.shape)})")
     return t.shape
+
+
+def _scratch(workspace, nbytes, like):
+    """(tensor, pointer, bytes) of the workspace; the tensor keeps it alive."""
+    if nbytes == 0:
+        return None, None, 0
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), nbytes
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _elsewhere(t, stream):
+    """The context that makes t's device, and ``stream`` if there is one,
+    current; None where they are already."""
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a CUDA device (got {t.device})")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.get_device() != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return None
+
+
+def _stream_of(t):
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, max_new, page_summary=None, q=None,
@@ -378,35 +382,45 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
     are rotated by their positions; without it k is stored as given.
     ``page_summary`` [n_pages, Hkv, 2, D], if given, is kept up to date.
     Returns the rotated q (``q_out``; it may be q itself) or None."""
-    T, Hkv, D = _heads3("k", k)
-    device, dtype = k.device, k.dtype
+    elsewhere = _elsewhere(k, stream) if k.is_cuda else None
+    if elsewhere is not None:
+        with elsewhere:
+            return jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, max_new, page_summary, q,
+                                   q_out, rope_theta)
+    T, Hkv, D = shape = _heads3("k", k)
+    dtype = k.dtype
     code = _dtype_code(k)
     B = seqlens.numel()
-    _tensor("k", k, (T, Hkv, D), dtype, device)
-    _tensor("v", v, (T, Hkv, D), dtype, device)
-    page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, dtype, device)
-    cols, table_stride = _table(block_table, B, device)
-    _tensor("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, device)
-    _tensor("seqlens", seqlens, (B,), torch.int32, device)
+    _tensor("k", k, shape, dtype, k)
+    _tensor("v", v, shape, dtype, k)
+    page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, k)
+    cols, table_stride = _table(block_table, B, k)
+    _tensor("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, k)
+    _tensor("seqlens", seqlens, (B,), torch.int32, k)
+    summary = q_in = q_to = None
     if page_summary is not None:
-        _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, device)
-    if rope_theta is None and q is not None:
-        raise ValueError("q is only rotated: it needs rope_theta")
-    if q is None and q_out is not None:
-        raise ValueError("q_out without q")
+        _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, k)
+        summary = page_summary.data_ptr()
     Hq = Hkv
     if q is not None:
+        if rope_theta is None:
+            raise ValueError("q is only rotated: it needs rope_theta")
         Hq = _heads3("q", q)[1]
-        _tensor("q", q, (T, Hq, D), dtype, device)
-    with _On(device, stream) as st:
-        if q is not None:
-            q_out = _given("q_out", q_out, (T, Hq, D), dtype, device)
-        _check(lib().jl_paged_append(
-            k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            None if page_summary is None else page_summary.data_ptr(), block_table.data_ptr(), table_stride, cols,
-            cu_seqlens.data_ptr(), seqlens.data_ptr(), B, T, int(max_new), Hq, Hkv, D, page, n_pages, page_stride,
-            None if q is None else q.data_ptr(), None if q is None else q_out.data_ptr(),
-            0.0 if rope_theta is None else float(rope_theta), code, 0 if rope_theta is None else JL_FLAG_ROTATE, st))
+        _tensor("q", q, (T, Hq, D), dtype, k)
+        if q_out is not None:
+            _tensor("q_out", q_out, (T, Hq, D), dtype, k)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _elsewhere(k, None)
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        q_in, q_to = q.data_ptr(), q_out.data_ptr()
+    theta, flags = (0.0, 0) if rope_theta is None else (rope_theta, JL_FLAG_ROTATE)
+    _check(lib().jl_paged_append(
+        k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), summary, block_table.data_ptr(),
+        table_stride, cols, cu_seqlens.data_ptr(), seqlens.data_ptr(), B, T, int(max_new), Hq, Hkv, D, page, n_pages,
+        page_stride, q_in, q_to, float(theta), code, flags, _stream_of(k)))
     return q_out
 
 
@@ -420,26 +434,33 @@ def jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_
     first, the ``n_last`` newest and the highest scored others of every kv
     head, ascending, -1 behind the last: int32 [B, Hkv, n_select], for
     jl_bifocal_decode_paged.  q [B, Hq, D] at position seqlens[b] - 1."""
+    elsewhere = _elsewhere(q, stream) if q.is_cuda else None
+    if elsewhere is not None:
+        with elsewhere:
+            return jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_select, w_pretrained,
+                                           w0, rope_theta, n_first, n_last, out, flags, workspace)
     B, Hq, D = _heads3("q", q)
-    device, dtype = q.device, q.dtype
+    dtype = q.dtype
     code = _dtype_code(q)
     if page_summary.dim() != 4:
         raise ValueError(f"page_summary must be [n_pages, Hkv, 2, D] (got {list(page_summary.shape)})")
-    n_pages, Hkv = page_summary.shape[0], page_summary.shape[1]
-    n_select = int(n_select)
-    _tensor("q", q, (B, Hq, D), dtype, device)
-    _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, device)
-    cols, table_stride = _table(block_table, B, device)
-    _tensor("seqlens", seqlens, (B,), torch.int32, device)
+    n_pages, Hkv, n_select = page_summary.shape[0], page_summary.shape[1], int(n_select)
+    _tensor("q", q, (B, Hq, D), dtype, q)
+    _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, q)
+    cols, table_stride = _table(block_table, B, q)
+    _tensor("seqlens", seqlens, (B,), torch.int32, q)
+    if out is not None:
+        _tensor("out", out, (B, Hkv, n_select), torch.int32, q)
+    _elsewhere(q, None)
     L = lib()
-    with _On(device, stream) as st:
-        out = _given("out", out, (B, Hkv, max(n_select, 0)), torch.int32, device)
-        need = L.jl_bifocal_select_pages_workspace_size(B, Hkv, cols, n_select)
-        keep, ws, ws_bytes = _scratch(workspace, need, device)
-        _check(L.jl_bifocal_select_pages(
-            q.data_ptr(), page_summary.data_ptr(), block_table.data_ptr(), table_stride, cols, seqlens.data_ptr(),
-            B, Hq, Hkv, D, int(page_size), n_pages, n_select, int(n_first), int(n_last), int(w_pretrained), int(w0),
-            float(rope_theta), out.data_ptr(), ws, ws_bytes, code, int(flags), st))
+    if out is None:
+        out = torch.empty((B, Hkv, max(n_select, 0)), dtype=torch.int32, device=q.device)
+    need = L.jl_bifocal_select_pages_workspace_size(B, Hkv, cols, n_select)
+    keep, ws, ws_bytes = _scratch(workspace, need, q)
+    _check(L.jl_bifocal_select_pages(
+        q.data_ptr(), page_summary.data_ptr(), block_table.data_ptr(), table_stride, cols, seqlens.data_ptr(),
+        B, Hq, Hkv, D, int(page_size), n_pages, n_select, int(n_first), int(n_last), int(w_pretrained), int(w0),
+        float(rope_theta), out.data_ptr(), ws, ws_bytes, code, int(flags), _stream_of(q)))
     return out
 
 
@@ -453,31 +474,40 @@ def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrai
     seqlens[b] - 1 against the pages of block_table [B, max_pages]; only those
     of ``page_list`` [B, Hkv, n] if given, only the last ``window`` keys if
     not 0.  Returns (out [B, Hq, D], lse [B, Hq] or None)."""
-    B, Hq, D = _heads3("q", q)
-    device, dtype = q.device, q.dtype
+    elsewhere = _elsewhere(q, stream) if q.is_cuda else None
+    if elsewhere is not None:
+        with elsewhere:
+            return jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrained, w0, rope_theta,
+                                           page_list, window, out, lse, flags, workspace)
+    B, Hq, D = shape = _heads3("q", q)
+    dtype = q.dtype
     code = _dtype_code(q)
     if k_pages.dim() != 4:
         raise ValueError(f"k_pages must be [n_pages, page_size, Hkv, D] (got {list(k_pages.shape)})")
     Hkv = k_pages.shape[2]
-    _tensor("q", q, (B, Hq, D), dtype, device)
-    page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, dtype, device)
-    cols, table_stride = _table(block_table, B, device)
-    _tensor("seqlens", seqlens, (B,), torch.int32, device)
+    _tensor("q", q, shape, dtype, q)
+    page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, q)
+    cols, table_stride = _table(block_table, B, q)
+    _tensor("seqlens", seqlens, (B,), torch.int32, q)
     listed, n_list = None, 0
     if page_list is not None:
-        _tensor("page_list", page_list, (B, Hkv, -1), torch.int32, device)
+        n_list = page_list.shape[-1] if page_list.dim() == 3 else 0
+        _tensor("page_list", page_list, (B, Hkv, n_list), torch.int32, q)
         # an empty list's own pointer may be null: nothing of it is read
-        listed, n_list = page_list.data_ptr() or block_table.data_ptr(), page_list.shape[2]
+        listed = page_list.data_ptr() or block_table.data_ptr()
+    lse_to = None
     if lse is not None:
-        _tensor("lse", lse, (B, Hq), torch.float32, device)
+        _tensor("lse", lse, (B, Hq), torch.float32, q)
+        lse_to = lse.data_ptr()
+    if out is not None:
+        _tensor("out", out, shape, dtype, q)
+    _elsewhere(q, None)
     L = lib()
-    with _On(device, stream) as st:
-        out = _given("out", out, (B, Hq, D), dtype, device)
-        need = L.jl_bifocal_decode_paged_workspace_size(B, D)
-        keep, ws, ws_bytes = _scratch(workspace, need, device)
-        _check(L.jl_bifocal_decode_paged(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), table_stride, cols,
-            seqlens.data_ptr(), listed, n_list, B, Hq, Hkv, D, page, n_pages, page_stride, int(w_pretrained), int(w0),
-            int(window), float(rope_theta), out.data_ptr(), None if lse is None else lse.data_ptr(), ws, ws_bytes,
-            code, int(flags), st))
+    if out is None:
+        out = torch.empty_like(q)
+    keep, ws, ws_bytes = _scratch(workspace, L.jl_bifocal_decode_paged_workspace_size(B, D), q)
+    _check(L.jl_bifocal_decode_paged(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), table_stride, cols,
+        seqlens.data_ptr(), listed, n_list, B, Hq, Hkv, D, page, n_pages, page_stride, int(w_pretrained), int(w0),
+        int(window), float(rope_theta), out.data_ptr(), lse_to, ws, ws_bytes, code, int(flags), _stream_of(q)))
     return out, lse
