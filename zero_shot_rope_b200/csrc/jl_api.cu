@@ -437,7 +437,7 @@ jl_status jl_bifocal_select_pages(const void *q, const void *page_summary, const
   a.plain = (flags & JL_FLAG_PLAIN_CAUSAL) ? 1 : 0;
   a.list = page_list;
   a.score = (float *)workspace;
-  a.mx = (float *)((char *)workspace + align256(n * sizeof(float)));
+  a.size = (float *)((char *)workspace + align256(n * sizeof(float)));
   a.mark = (float *)((char *)workspace + 2 * align256(n * sizeof(float)));
   a.amb = (int32_t *)((char *)workspace + 3 * align256(n * sizeof(float)));
   a.fine = (double *)((char *)workspace + 4 * align256(n * sizeof(float)));

@@ -309,11 +309,10 @@ struct PagedSelectArgs {
   long long w_pre;
   int w0, plain;
   int32_t *list;
-  // [B, Hkv, max_pages] each: a page's fp32 score; the largest |min|, |max| of a
-  // group of mx_pages pages; 1 for a chosen page; the undecided pages and their
-  // scores in 64 bits
-  float *score, *mx, *mark;
-  int mx_pages;
+  // [B, Hkv, max_pages] each: a page's fp32 score (twice it); for pairs of pages,
+  // a bound of the sum of squares of their key ranges; 1 for a chosen page; the
+  // undecided pages and their scores in 64 bits
+  float *score, *size, *mark;
   int32_t *amb;
   double *fine;
 };

@@ -20,7 +20,6 @@ namespace jl {
 namespace pgs {
 
 constexpr int NT_SCORE = 256;
-constexpr int NT_SEL = 512;
 
 // PPL pairs per lane, as fp32: elements PPL l .. of a row's halves
 template <typename T, int PPL>
@@ -62,90 +61,205 @@ __device__ __forceinline__ int pool_page(const PagedSelectArgs &p, int b, int c)
   return page >= 0 && page < p.n_pages ? page : -1;
 }
 
-// Scores in fp32.  A CTA takes 16 pages of a sequence: first their angles, once
-// for all heads, then warps go through the kv heads with the head's queries in
-// registers, UP pages at a time.  UP pages x GP heads are 16 sums (or fewer) per
-// lane, which are added up over the lanes together: with each shuffle a lane
-// hands over half of what it holds and keeps the other half.
-constexpr int SCORE_PAGES = 16;
-__host__ __device__ constexpr int pages_at_once(int gp) { return gp <= 4 ? 4 : 2; }
+// packed fp32 pairs
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t d) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
+  return f;
+}
+// N values (2 or 4) from 2 N or 4 N aligned bytes
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T *p, float (&x)[N]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float2 v = *reinterpret_cast<const float2 *>(p + e);
+      x[e] = v.x, x[e + 1] = v.y;
+    }
+  } else {
+    uint32_t w[N / 2];
+    if constexpr (N == 4) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+#pragma unroll
+    for (int e = 0; e < N; e += 2) x[e] = __uint_as_float(w[e / 2] << 16), x[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
+  }
+}
+
+// Twice the scores, in fp32.  A CTA takes the key ranges of up to 16 pages and 8
+// kv heads, 64 KB at most, all asked for at once (a page's heads lie side by
+// side); the pages' angles are formed meanwhile, once for all heads.  Then warps
+// go through the heads with the head's queries in registers, two pages at a
+// time, one per half warp.  A lane has the sums of GP heads, which are added up
+// over the lanes together: with each shuffle it hands over half of what it holds
+// and keeps the other half.
+constexpr int SCORE_HEADS = 8;
+template <typename T, int D>
+__host__ __device__ constexpr int score_pages() { return 2 * D * sizeof(T) <= 512 ? 16 : 8; }
+template <typename T, int D>
+__host__ __device__ constexpr size_t score_smem() { return score_pages<T, D>() * SCORE_HEADS * 2 * D * sizeof(T); }
 
 template <typename T, int D, int GP>
-__global__ void __launch_bounds__(NT_SCORE)
+__global__ void __launch_bounds__(NT_SCORE, 2)
 score_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__ TurnFreq turn) {
-  constexpr int PPL = D / 64, HALF = D / 2, UP = pages_at_once(GP), NV = UP * GP, NW = NT_SCORE / 32;
-  __shared__ __align__(16) float2 ang[SCORE_PAGES][HALF];
-  __shared__ int pool[SCORE_PAGES];
-  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * SCORE_PAGES;
+  constexpr int HALF = D / 2, PPL = HALF / 16, NW = NT_SCORE / 32, SP = score_pages<T, D>();
+  extern __shared__ __align__(16) uint8_t range_s[];  // [SP][heads][2][D]
+  __shared__ float4 ang[SP][HALF / 2];                // of two neighbouring pairs: cos, cos, sin, sin
+  __shared__ const uint8_t *from_s[SP];  // a page's ranges, NULL: not there
+  __shared__ int turn_s[SP], np_s;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * SP;
+  const int h_first = blockIdx.z * SCORE_HEADS, heads = min(SCORE_HEADS, p.Hkv - h_first);
   let_next_kernel_come();
   wait_for_kernel_before();
-  const Seq s = seq_of(p, b);
-  if (s.pages <= p.n_select) return;  // all of them are listed
-  if (c0 >= s.pages) return;
-  if (threadIdx.x < SCORE_PAGES)
-    pool[threadIdx.x] = c0 + threadIdx.x < s.pages ? pool_page(p, b, c0 + threadIdx.x) : -1;
-#pragma unroll
-  for (int x = threadIdx.x; x < SCORE_PAGES * HALF; x += NT_SCORE) {
-    const int c = x / HALF, k = x % HALF;
-    float co, si;
-    turn_cs(c0 + c < s.pages ? page_turn(p, s, c0 + c) : 0, turn.v[k], co, si);
-    ang[c][k] = make_float2(co, si);
+  if (warp == 0) {
+    const int c = c0 + lane;
+    const int page = lane < SP && c < p.max_pages ? pool_page(p, b, c) : -1;
+    const Seq s = seq_of(p, b);
+    const int np = s.pages <= p.n_select ? 0 : min(SP, s.pages - c0);  // no more pages than the list: all of them are in it
+    if (lane < SP) {
+      turn_s[lane] = lane < np ? page_turn(p, s, c) : 0;
+      from_s[lane] = lane < np && page >= 0
+                         ? (const uint8_t *)p.summary + ((size_t)page * p.Hkv + h_first) * 2 * D * sizeof(T)
+                         : nullptr;
+    }
+    if (lane == 0) np_s = np;
   }
   __syncthreads();
-  const T *q = (const T *)p.q + (size_t)b * p.Hkv * p.GS * D;
-  const int per_head = SCORE_PAGES / UP;
-  const long long units = (long long)p.Hkv * per_head;
-  const int u1 = (int)(units * (warp + 1) / NW);
-  float qa[GP][PPL], qb[GP][PPL];
-  int held = -1;  // the head whose queries they are
-  for (int u = (int)(units * warp / NW); u < u1; ++u) {
-    const int h = u / per_head, x0 = (u % per_head) * UP;
-    if (c0 + x0 >= s.pages) continue;
-    float la[UP][PPL], lb[UP][PPL], ha[UP][PPL], hb[UP][PPL];
-    uint32_t mx = 0;
+  const int np = np_s;
+  if (np <= 0) return;
+  {
+    const int per = heads * 2 * D * (int)sizeof(T);  // bytes of a page
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(range_s);
 #pragma unroll
-    for (int x = 0; x < UP; ++x) {
-      const int page = pool[x0 + x];
-      if (page >= 0) {
-        const T *row = (const T *)p.summary + ((size_t)page * p.Hkv + h) * 2 * D;
-        load_pairs<T, PPL>(row, HALF, lane, la[x], lb[x]);
-        load_pairs<T, PPL>(row + D, HALF, lane, ha[x], hb[x]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < PPL; ++e) la[x][e] = lb[x][e] = ha[x][e] = hb[x][e] = 0.f;
+    for (int c = 0; c < SP; ++c) {
+      const uint8_t *from = from_s[c];
+      for (int x = threadIdx.x * 16; x < per; x += NT_SCORE * 16) {  // a page that is not there: zeros
+        const bool there = from != nullptr;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + c * per + x),
+                     "l"(there ? from + x : (const uint8_t *)p.summary), "r"(there ? 16 : 0)
+                     : "memory");
       }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+#pragma unroll
+  for (int x = threadIdx.x; x < SP * HALF; x += NT_SCORE) {
+    const int c = x / HALF, k = x % HALF;
+    float co, si;
+    turn_cs(turn_s[c], turn.v[k], co, si);
+    float *to = reinterpret_cast<float *>(&ang[c][k / 2]) + (k & 1);
+    to[0] = co;
+    to[2] = si;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  const T *q = (const T *)p.q + (size_t)b * p.Hkv * p.GS * D;
+  const int sub = lane >> 4, k0 = (lane & 15) * PPL;  // page of the two, first pair of this lane
+  // a unit: two pages of a head; a warp takes a run of units, head by head
+  const int per_head = SP / 2, units = heads * per_head, u1 = units * (warp + 1) / NW;
+  uint64_t qa[GP][PPL / 2], qb[GP][PPL / 2];
+  int held = -1;         // the head whose queries they are
+  float size[2 * PPL];   // the largest |min|, |max| of each channel over the pages of that head seen so far
+  auto put_size = [&](int h, int first, int n) {  // of page pairs first .. first + n - 1 of the CTA
+    float sq = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2 * PPL; ++e) {
+      size[e] = max_nan(size[e], __shfl_xor_sync(0xffffffffu, size[e], 16));
+      sq = fmaf(size[e], size[e], sq);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane < n && 2 * (first + lane) < np) p.size[((size_t)b * p.Hkv + h) * p.max_pages + c0 / 2 + first + lane] = sq;
+  };
+  auto load_q = [&](int h, int g0) {
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {  // a head twice is no other maximum
+      const T *row = q + (size_t)(h * p.GS + min(g0 + g, p.GS - 1)) * D + k0;
+      float x[PPL], y[PPL];
+      load_n<T, PPL>(row, x);
+      load_n<T, PPL>(row + HALF, y);
+#pragma unroll
+      for (int e = 0; e < PPL / 2; ++e) qa[g][e] = pack2(x[2 * e], x[2 * e + 1]), qb[g][e] = pack2(y[2 * e], y[2 * e + 1]);
+    }
+  };
+  for (int u = units * warp / NW; u < u1; ++u) {
+    const int h = h_first + u / per_head, x0 = (u % per_head) * 2;
+    if (held != h) {
+      held = h;
+      load_q(h, 0);
+#pragma unroll
+      for (int e = 0; e < 2 * PPL; ++e) size[e] = 0.f;
+    }
+    const int x = x0 + sub;
+    // 2 max(t lo, t hi) = t (hi + lo) + |t| (hi - lo)
+    uint64_t mid_a[PPL / 2], mid_b[PPL / 2], rad_a[PPL / 2], rad_b[PPL / 2];
+    {
+      const T *row = reinterpret_cast<const T *>(range_s) + (x * heads + h - h_first) * 2 * D + k0;
+      float la[PPL], lb[PPL], ha[PPL], hb[PPL];
+      load_n<T, PPL>(row, la);
+      load_n<T, PPL>(row + HALF, lb);
+      load_n<T, PPL>(row + D, ha);
+      load_n<T, PPL>(row + D + HALF, hb);
+#pragma unroll
+      for (int e = 0; e < PPL; ++e) {
+        size[2 * e] = max_nan(size[2 * e], max_nan(fabsf(la[e]), fabsf(ha[e])));
+        size[2 * e + 1] = max_nan(size[2 * e + 1], max_nan(fabsf(lb[e]), fabsf(hb[e])));
+      }
+#pragma unroll
+      for (int e = 0; e < PPL / 2; ++e) {
+        mid_a[e] = pack2(ha[2 * e] + la[2 * e], ha[2 * e + 1] + la[2 * e + 1]);
+        rad_a[e] = pack2(ha[2 * e] - la[2 * e], ha[2 * e + 1] - la[2 * e + 1]);
+        mid_b[e] = pack2(hb[2 * e] + lb[2 * e], hb[2 * e + 1] + lb[2 * e + 1]);
+        rad_b[e] = pack2(hb[2 * e] - lb[2 * e], hb[2 * e + 1] - lb[2 * e + 1]);
+      }
+    }
+    uint64_t co[PPL / 2], si[PPL / 2], ns[PPL / 2];
+#pragma unroll
+    for (int e = 0; e < PPL / 2; ++e) {
+      const float4 f = ang[x][k0 / 2 + e];
+      co[e] = pack2(f.x, f.y), si[e] = pack2(f.z, f.w), ns[e] = si[e] ^ 0x8000000080000000ull;
     }
     float best = -INFINITY;
     for (int g0 = 0; g0 < p.GS; g0 += GP) {
-      if (held != h || p.GS > GP) {
+      if (p.GS > GP) load_q(h, g0);
+      float v[GP];
 #pragma unroll
-        for (int g = 0; g < GP; ++g)  // a head twice is no other maximum
-          load_pairs<T, PPL>(q + (size_t)(h * p.GS + min(g0 + g, p.GS - 1)) * D, HALF, lane, qa[g], qb[g]);
-        held = h;
-      }
-      float v[NV];
+      for (int g = 0; g < GP; ++g) {
+        uint64_t y = 0ull;
 #pragma unroll
-      for (int x = 0; x < UP; ++x) {
-        float2 cs[PPL];
-#pragma unroll
-        for (int e = 0; e < PPL; ++e) cs[e] = ang[x0 + x][PPL * lane + e];
-#pragma unroll
-        for (int g = 0; g < GP; ++g) {
-          float y = 0.f;
-#pragma unroll
-          for (int e = 0; e < PPL; ++e) {
-            // <R(-turn) k, q> = <k, R(turn) q>
-            const float ta = fmaf(qa[g][e], cs[e].x, -(qb[g][e] * cs[e].y));
-            const float tb = fmaf(qb[g][e], cs[e].x, qa[g][e] * cs[e].y);
-            y = fmaf(ta, ta >= 0.f ? ha[x][e] : la[x][e], y);
-            y = fmaf(tb, tb >= 0.f ? hb[x][e] : lb[x][e], y);
-          }
-          v[x * GP + g] = y;
+        for (int e = 0; e < PPL / 2; ++e) {
+          // <R(-turn) k, q> = <k, R(turn) q>
+          const uint64_t ta = fma2(qa[g][e], co[e], mul2(qb[g][e], ns[e]));
+          const uint64_t tb = fma2(qb[g][e], co[e], mul2(qa[g][e], si[e]));
+          y = fma2(ta, mid_a[e], y);
+          y = fma2(tb, mid_b[e], y);
+          y = fma2(ta & 0x7fffffff7fffffffull, rad_a[e], y);
+          y = fma2(tb & 0x7fffffff7fffffffull, rad_b[e], y);
         }
+        const float2 f = unpack2(y);
+        v[g] = f.x + f.y;
       }
-      int o = 16;
+      int o = 8;
 #pragma unroll
-      for (int n = NV; n > 1; n >>= 1, o >>= 1)
+      for (int n = GP; n > 1; n >>= 1, o >>= 1)
 #pragma unroll
         for (int i = 0; i < n / 2; ++i) {
           const bool up = lane & o;
@@ -159,20 +273,13 @@ score_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__ 
     }
     // lane bits from the top: page, head, copies
 #pragma unroll
-    for (int o = 16 / UP; o > 16 / NV; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-#pragma unroll
-    for (int x = 0; x < UP; ++x)
-#pragma unroll
-      for (int e = 0; e < PPL; ++e) {
-        // magnitudes as bits: a NaN stays above every number
-        mx = max(max(mx, __float_as_uint(fabsf(la[x][e]))), __float_as_uint(fabsf(ha[x][e])));
-        mx = max(max(mx, __float_as_uint(fabsf(lb[x][e]))), __float_as_uint(fabsf(hb[x][e])));
-      }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    const size_t at = ((size_t)b * p.Hkv + h) * p.max_pages;
-    const int x = lane / (32 / UP);
-    if (lane % (32 / UP) == 0 && c0 + x0 + x < s.pages) p.score[at + c0 + x0 + x] = pool[x0 + x] >= 0 ? best : -INFINITY;
-    if (lane == 0) p.mx[at + (c0 + x0) / UP] = __uint_as_float(mx);
+    for (int o = 8; o > 8 / GP; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if ((lane & 15) == 0 && x < np)
+      p.score[((size_t)b * p.Hkv + h) * p.max_pages + c0 + x] = from_s[x] != nullptr ? best : -INFINITY;
+    if (u + 1 == u1 || (u + 1) % per_head == 0) {  // the warp's last unit of this head
+      const int first = max(units * warp / NW - (h - h_first) * per_head, 0);
+      put_size(h, first, x0 / 2 + 1 - first);
+    }
   }
 }
 
@@ -186,6 +293,14 @@ __device__ double score64(const PagedSelectArgs &p, const InvFreq &inv, const Se
   const T *row = (const T *)p.summary + ((size_t)page * p.Hkv + h) * 2 * D;
   const T *q = (const T *)p.q + ((size_t)b * p.Hkv + h) * p.GS * D;
   const int turn = page_turn(p, s, c);
+  double cs[PPL], sn[PPL], lo[2 * PPL], hi[2 * PPL];
+#pragma unroll
+  for (int e = 0; e < PPL; ++e) {
+    const int k = PPL * lane + e;
+    sincos_fp64((double)turn * inv.v[k], sn[e], cs[e]);
+    lo[2 * e] = to_f(row[k]), hi[2 * e] = to_f(row[D + k]);
+    lo[2 * e + 1] = to_f(row[HALF + k]), hi[2 * e + 1] = to_f(row[D + HALF + k]);
+  }
   double best = -INFINITY;
   for (int g = 0; g < p.GS; ++g) {
     double x = 0.0;
@@ -193,12 +308,9 @@ __device__ double score64(const PagedSelectArgs &p, const InvFreq &inv, const Se
 #pragma unroll
     for (int e = 0; e < PPL; ++e) {
       const int k = PPL * lane + e;
-      double sn, cs;
-      sincos_fp64((double)turn * inv.v[k], sn, cs);
       const double qa = to_f(q[(size_t)g * D + k]), qb = to_f(q[(size_t)g * D + HALF + k]);
-      const double ta = qa * cs - qb * sn, tb = qb * cs + qa * sn;
-      const double pa = ta * to_f(row[k]), pb = ta * to_f(row[D + k]);
-      const double pc = tb * to_f(row[HALF + k]), pd = tb * to_f(row[D + HALF + k]);
+      const double ta = qa * cs[e] - qb * sn[e], tb = qb * cs[e] + qa * sn[e];
+      const double pa = ta * lo[2 * e], pb = ta * hi[2 * e], pc = tb * lo[2 * e + 1], pd = tb * hi[2 * e + 1];
       x += (pa > pb ? pa : pb) + (pc > pd ? pc : pd);
       bad = bad || isnan(pa) || isnan(pb) || isnan(pc) || isnan(pd);
     }
@@ -225,7 +337,7 @@ __device__ __forceinline__ float unorder(uint32_t k) {
 
 // The k-th largest (k >= 1) of the keys key(0 .. n-1), by the whole block: one
 // digit of eight bits at a time, from the top.  *above: how many are larger.
-template <typename K, typename F>
+template <int NT_SEL, typename K, typename F>
 __device__ K kth_largest(F key, int n, int k, int *above) {
   __shared__ int hist[256];
   __shared__ int s_digit, s_left;
@@ -270,6 +382,7 @@ __device__ K kth_largest(F key, int n, int k, int *above) {
 }
 
 // exclusive prefix sum of x over the block; *total: the sum
+template <int NT_SEL>
 __device__ int block_scan(int x, int *total) {
   __shared__ int s_warp[NT_SEL / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -295,7 +408,7 @@ __device__ int block_scan(int x, int *total) {
 // Of R keys per thread (whole numbers, 0: none): the k-th largest, by the whole
 // block, two bits at a time from the top.  Once exactly k keys are at or above
 // a threshold, the least of them is it.
-template <int R>
+template <int NT_SEL, int R>
 __device__ uint32_t kth_largest_held(const uint32_t (&key)[R], int k) {
   constexpr int NW = NT_SEL / 32;
   __shared__ uint64_t s_count[2][NW];
@@ -338,21 +451,25 @@ __device__ uint32_t kth_largest_held(const uint32_t (&key)[R], int k) {
 // a page scored above T + 2 eps is surely chosen, one below T - 2 eps surely
 // not, and the few between are decided by their scores in 64 bits (equal ones:
 // the lower page first).  Where all of those are needed anyway, as nearly
-// always, nothing is left to decide; a sequence of up to R x 512 pages then has
-// its scores read once and kept in registers.
+// always, nothing is left to decide; a sequence of up to R pages per thread then
+// has its scores read once and kept in registers.
 //
-// eps: with Mx the largest |min|, |max| of a page and Q the sum over channels
-// of the length of the query's pair (which no rotation changes), a score is a
-// sum of D terms |q'_d m_d| whose sizes add up to at most Q Mx.  Relative to
-// that, with u = 2^-24: the turned query is off by at most 7u (cosine and sine
-// within 3u, one product, one sum), taking the wrong side of a q' within its own
-// error of zero costs at most 14u, and a term goes through at most 4 + 5 further
-// roundings: 30u < 2^-19.  2^-18 is used: Q, Mx and the thresholds are rounded too.
-template <typename T, int D, int R>
+// eps: a score is a sum of D terms |q'_d m_d|, m_d the larger of |min_d| and
+// |max_d|, whose sizes add up to at most |q| |m| (2-norms; turning leaves |q|
+// as it is).  Relative to that, with u = 2^-24: the turned query is off by at
+// most 7u (cosine and sine within 3u, one product, one sum), hi + lo and
+// hi - lo by 1u each, and a term goes through at most 8 + 5 further sums:
+// 22u = 1.32e-6.  1.9e-6 is used (and twice that for twice the score), as the norms and thresholds are rounded too;
+// 2e-18 makes up for squares and 1e-36 for products below the normal range.
+template <typename T, int D, int NT_SEL, int R>
 __global__ void __launch_bounds__(NT_SEL)
 select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__ InvFreq inv) {
   constexpr int NW = NT_SEL / 32;
+  constexpr int FEW = 64;  // undecided pages that are settled in shared memory
   __shared__ float s_max[2][NW];
+  __shared__ int s_und[FEW];
+  __shared__ double s_fine[FEW];
+  __shared__ bool s_take[FEW];
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_kernel_come();
   wait_for_kernel_before();
@@ -377,22 +494,19 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
   float above_t = INFINITY, below_t = INFINITY;  // chosen above the one, undecided from the other on
   if (k > 0) {
     // eps
-    uint32_t mx = 0;
-    const int groups = (s.pages + p.mx_pages - 1) / p.mx_pages;
-    for (int x = tid; x < groups; x += NT_SEL) mx = max(mx, __float_as_uint(p.mx[row * p.max_pages + x]));
+    float size = 0.f;
+    for (int x = tid; x < (s.pages + 1) / 2; x += NT_SEL) size = max_nan(size, p.size[row * p.max_pages + x]);
     float qs = 0.f;
     const T *q = (const T *)p.q + row * p.GS * D;
     for (int g = warp; g < p.GS; g += NW) {
       float x = 0.f;
 #pragma unroll
-      for (int d = lane; d < D / 2; d += 32) {
-        const float u = to_f(q[g * D + d]), v = to_f(q[g * D + D / 2 + d]);
-        x += 2.f * sqrtf(u * u + v * v);
-      }
+      for (int d = lane; d < D; d += 32) x = fmaf(to_f(q[g * D + d]), to_f(q[g * D + d]), x);
       qs = max_nan(qs, warp_sum(x));
     }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 0) s_max[0][warp] = __uint_as_float(mx), s_max[1][warp] = qs;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) size = max_nan(size, __shfl_xor_sync(0xffffffffu, size, o));
+    if (lane == 0) s_max[0][warp] = size, s_max[1][warp] = qs;
     float t;
     if (held) {
 #pragma unroll
@@ -400,17 +514,17 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
         const int c = R * tid + x;
         key[x] = c >= lo && c < lo + n ? order_key(mine[x]) : 0u;
       }
-      t = unorder(kth_largest_held<R>(key, k));
+      t = unorder(kth_largest_held<NT_SEL, R>(key, k));
     } else {
       int above;
-      t = unorder(kth_largest<uint32_t>([&](int x) { return order_key(score[lo + x]); }, n, k, &above));
+      t = unorder(kth_largest<NT_SEL, uint32_t>([&](int x) { return order_key(score[lo + x]); }, n, k, &above));
     }
     __syncthreads();
-    float Mx = 0.f, Q = 0.f;
+    float m2 = 0.f, q2 = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) Mx = max_nan(Mx, s_max[0][w]), Q = max_nan(Q, s_max[1][w]);
-    const float eps = 3.9e-6f * Q * Mx + 1e-36f;  // (1e-36: products below the normal range)
-    if (eps < 1e30f) {                            // no score near overflow, and nothing infinite or NaN
+    for (int w = 0; w < NW; ++w) m2 = max_nan(m2, s_max[0][w]), q2 = max_nan(q2, s_max[1][w]);
+    const float eps = 3.8e-6f * (sqrtf(q2) + 2e-18f) * (sqrtf(m2) + 2e-18f) + 1e-36f;
+    if (eps < 1e30f) {  // no square or score near overflow, nothing infinite or NaN
       above_t = t + 2.f * eps;
       below_t = t - 2.f * eps;
     } else {  // fp32 says nothing here: all undecided
@@ -418,21 +532,53 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
     }
   }
   if (held) {
-    bool yes[R];
+    bool yes[R], near_s[R];
     int sure = 0, maybe = 0;
 #pragma unroll
     for (int x = 0; x < R; ++x) {
       const int c = R * tid + x;
       const bool in = c < s.pages, forced = in && (c < lo || c >= lo + n);
       const bool top = in && k > 0 && mine[x] > above_t, near = in && k > 0 && !top && mine[x] >= below_t;
+      near_s[x] = near && !forced;
       yes[x] = forced || top || near;
       sure += forced || top;
-      maybe += !forced && near;
+      maybe += near_s[x];
     }
     int both;
-    const int at = block_scan(sure | maybe << 16, &both);
+    const int at = block_scan<NT_SEL>(sure | maybe << 16, &both);
     if ((both & 0xffff) + (both >> 16) == p.n_select) {
       int out = (at & 0xffff) + (at >> 16);
+#pragma unroll
+      for (int x = 0; x < R; ++x)
+        if (yes[x]) list[out++] = R * tid + x;
+      return;
+    }
+    const int und = both >> 16, need = p.n_select - (both & 0xffff);
+    if (und <= FEW) {
+      int x1 = at >> 16;
+#pragma unroll
+      for (int x = 0; x < R; ++x)
+        if (near_s[x]) s_und[x1++] = R * tid + x;
+      __syncthreads();
+      for (int x = warp; x < und; x += NW) {
+        const double v = score64<T, D>(p, inv, s, b, h, s_und[x], lane);
+        if (lane == 0) s_fine[x] = v;
+      }
+      __syncthreads();
+      if (tid < und) {  // in ascending order of page: the lower wins a tie
+        int rank = 0;
+        for (int y = 0; y < und; ++y) rank += s_fine[y] > s_fine[tid] || (s_fine[y] == s_fine[tid] && y < tid);
+        s_take[tid] = rank < need;
+      }
+      __syncthreads();
+      x1 = at >> 16;
+      int n_yes = 0;
+#pragma unroll
+      for (int x = 0; x < R; ++x) {
+        if (near_s[x]) yes[x] = s_take[x1++];
+        n_yes += yes[x];
+      }
+      int sum, out = block_scan<NT_SEL>(n_yes, &sum);
 #pragma unroll
       for (int x = 0; x < R; ++x)
         if (yes[x]) list[out++] = R * tid + x;
@@ -454,10 +600,10 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
       mark[c] = yes ? 1.f : 0.f;
     }
     int sum;
-    const int at = block_scan(maybe ? 1 : 0, &sum);
+    const int at = block_scan<NT_SEL>(maybe ? 1 : 0, &sum);
     if (maybe) amb[und + at] = c;
     und += sum;
-    block_scan(yes ? 1 : 0, &sum);
+    block_scan<NT_SEL>(yes ? 1 : 0, &sum);
     sure += sum;
   }
   __syncthreads();
@@ -471,14 +617,14 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
     }
     __syncthreads();
     int above;
-    const uint64_t kt = kth_largest<uint64_t>([&](int x) { return order_key(fine[x]); }, und, need, &above);
+    const uint64_t kt = kth_largest<NT_SEL, uint64_t>([&](int x) { return order_key(fine[x]); }, und, need, &above);
     int equal = need - above;  // of those equal to the last chosen, the first
     for (int x0 = 0; x0 < und; x0 += NT_SEL) {
       const int x = x0 + tid;
       const uint64_t v = x < und ? order_key(fine[x]) : 0;
       const bool eq = x < und && v == kt;
       int sum;
-      const int at = block_scan(eq ? 1 : 0, &sum);
+      const int at = block_scan<NT_SEL>(eq ? 1 : 0, &sum);
       if (x < und && (v > kt || (eq && at < equal))) mark[amb[x]] = 1.f;
       equal -= min(equal, sum);
     }
@@ -489,7 +635,7 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
     const int c = x0 + tid;
     const bool yes = c < s.pages && mark[c] != 0.f;
     int sum;
-    const int at = block_scan(yes ? 1 : 0, &sum);
+    const int at = block_scan<NT_SEL>(yes ? 1 : 0, &sum);
     if (yes) list[out + at] = c;
     out += sum;
   }
@@ -499,18 +645,23 @@ template <typename T, int D>
 cudaError_t launch(const PagedSelectArgs &args, const InvFreq &inv, const TurnFreq &turn, cudaStream_t st) {
   PagedSelectArgs a = args;
   const int gp = a.GS == 1 ? 1 : a.GS == 2 ? 2 : a.GS <= 4 ? 4 : 8;
-  a.mx_pages = pages_at_once(gp);
   if (a.max_pages > a.n_select) {  // some sequence may have more pages than the list
     const auto kernel = gp == 1   ? score_kernel<T, D, 1>
                         : gp == 2 ? score_kernel<T, D, 2>
                         : gp == 4 ? score_kernel<T, D, 4>
                                   : score_kernel<T, D, 8>;
-    const cudaError_t e = launch_overlapped(kernel, dim3((a.max_pages + SCORE_PAGES - 1) / SCORE_PAGES, a.B), NT_SCORE, 0,
-                                            st, a, turn);
+    constexpr int SP = score_pages<T, D>();
+    const dim3 grid((a.max_pages + SP - 1) / SP, a.B, (a.Hkv + SCORE_HEADS - 1) / SCORE_HEADS);
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)score_smem<T, D>());
+    if (e == cudaSuccess) e = launch_overlapped(kernel, grid, NT_SCORE, score_smem<T, D>(), st, a, turn);
     if (e != cudaSuccess) return e;
   }
-  const auto kernel = a.max_pages <= 4 * NT_SEL ? select_kernel<T, D, 4> : select_kernel<T, D, 16>;
-  return launch_overlapped(kernel, dim3(a.Hkv, a.B), NT_SEL, 0, st, a, inv);
+  // few pages: few threads, whose barriers are short
+  const dim3 grid(a.Hkv, a.B);
+  if (a.max_pages <= 512) return launch_overlapped(select_kernel<T, D, 128, 4>, grid, 128, 0, st, a, inv);
+  if (a.max_pages <= 2048) return launch_overlapped(select_kernel<T, D, 512, 4>, grid, 512, 0, st, a, inv);
+  return launch_overlapped(select_kernel<T, D, 512, 16>, grid, 512, 0, st, a, inv);
 }
 
 }  // namespace pgs
