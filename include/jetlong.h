@@ -442,6 +442,19 @@ jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages,
                                   jl_dtype dtype, uint32_t flags,
                                   void *stream);
 
+/*
+ * jl_paged_call - one of the three calls above, its arguments in 64-bit words
+ * in the order of its declaration: pointers as they are, integers and enums
+ * sign-extended, rope_theta by its bits.  For bindings in which every argument
+ * of a foreign call has its price.  A word that does not fit its argument's
+ * type, or another number of words, is JL_ERR_INVALID_ARG.
+ */
+#define JL_CALL_PAGED_APPEND 0         /* 25 words */
+#define JL_CALL_BIFOCAL_SELECT_PAGES 1 /* 24 words */
+#define JL_CALL_BIFOCAL_DECODE_PAGED 2 /* 27 words */
+
+jl_status jl_paged_call(int32_t call, const int64_t *words, int32_t n_words);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

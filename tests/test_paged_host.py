@@ -270,3 +270,30 @@ def test_turns_match_64_bit_angles():
     assert worst <= 1.0, worst
     L.jl_debug_turn_cs(0, 1.0, ctypes.byref(c), ctypes.byref(s))
     assert c.value == 1.0 and s.value == 0.0
+
+
+def test_packed_call_checks_its_words():
+    import struct
+
+    jl = _lib()
+    L = jl.lib()
+
+    def call(which, words, n=None):
+        data = struct.pack(f"={len(words)}q", *words)
+        return jl.status_string(L.jl_paged_call(which, data, len(words) if n is None else n))
+
+    theta = struct.unpack("=q", struct.pack("=d", 1e4))[0]
+    append = [A, A, A, A, 0, A, 4, 4, A, A, 0, 8, 4, 4, 2, 128, 16, 10, 16 * 256, 0, 0, theta, 0, 0, 0]
+    select = [A, A, A, 40, 40, A, 0, 4, 2, 128, 16, 10, 8, 1, 1, 100, 10, theta, A, 1 << 20, 1 << 30, 0, 0, 0]
+    decode = [A, A, A, A, 40, 40, A, 0, 0, 0, 4, 2, 128, 16, 10, 16 * 256, 100, 10, 0, theta, A, 0, 1 << 20, 1 << 30, 0,
+              0, 0]
+    for which, words in enumerate((append, select, decode)):
+        assert call(which, words) == "JL_OK"          # an empty batch
+        assert call(which, words[:-1]) == "JL_ERR_INVALID_ARG"
+        assert call(which, words + [0]) == "JL_ERR_INVALID_ARG"
+        at = words.index(128)
+        assert call(which, words[:at] + [128 + (1 << 32)] + words[at + 1:]) == "JL_ERR_INVALID_ARG"
+        assert call(which, words[:at] + [96] + words[at + 1:]) == "JL_ERR_UNSUPPORTED"
+        assert call(which, words[:-2] + [-1, 0]) == "JL_ERR_INVALID_ARG"   # flags
+    assert call(3, append) == "JL_ERR_INVALID_ARG" and call(-1, append) == "JL_ERR_INVALID_ARG"
+    assert jl.status_string(L.jl_paged_call(0, None, 25)) == "JL_ERR_INVALID_ARG"

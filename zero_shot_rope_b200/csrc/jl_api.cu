@@ -517,6 +517,94 @@ jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void
   return e == cudaSuccess ? ok() : cuda_fail(e, "paged decode launch");
 }
 
+jl_status jl_paged_call(int32_t call, const int64_t *words, int32_t n_words) {
+  static const int32_t kWords[3] = {25, 24, 27};
+  if (call < 0 || call > 2 || words == nullptr || n_words != kWords[call])
+    return fail(JL_ERR_INVALID_ARG, "jl_paged_call: no such call, or not its number of words (%d, %d)", call, n_words);
+  bool fits = true;
+  int at = 0;
+  auto word = [&]() {
+    int64_t w;
+    memcpy(&w, reinterpret_cast<const char *>(words) + 8 * at++, 8);  // the words need not be aligned
+    return w;
+  };
+  auto ptr = [&]() { return reinterpret_cast<void *>(word()); };
+  auto i32 = [&]() {
+    const int64_t w = word();
+    fits = fits && w == (int32_t)w;
+    return (int32_t)w;
+  };
+  auto u32 = [&]() {
+    const int64_t w = word();
+    fits = fits && w == (int64_t)(uint32_t)w;
+    return (uint32_t)w;
+  };
+  auto f64 = [&]() {
+    const int64_t w = word();
+    double d;
+    memcpy(&d, &w, 8);
+    return d;
+  };
+  const char *kRange = "an argument does not fit 32 bits";
+  if (call == JL_CALL_PAGED_APPEND) {
+    const void *k = ptr(), *v = ptr();
+    void *kp = ptr(), *vp = ptr(), *sum = ptr();
+    const int32_t *table = (const int32_t *)ptr();
+    const int64_t stride = word();
+    const int32_t cols = i32();
+    const int32_t *cu = (const int32_t *)ptr(), *lens = (const int32_t *)ptr();
+    const int32_t batch = i32(), total = i32(), max_new = i32(), hq = i32(), hkv = i32(), d = i32(), page = i32(),
+                  n = i32();
+    const int64_t page_stride = word();
+    const void *q = ptr();
+    void *qo = ptr();
+    const double theta = f64();
+    const int32_t dtype = i32();
+    const uint32_t flags = u32();
+    void *stream = ptr();
+    if (!fits) return fail(JL_ERR_INVALID_ARG, "%s", kRange);
+    return jl_paged_append(k, v, kp, vp, sum, table, stride, cols, cu, lens, batch, total, max_new, hq, hkv, d, page, n,
+                           page_stride, q, qo, theta, (jl_dtype)dtype, flags, stream);
+  }
+  const void *q = ptr(), *k = ptr(), *v = call == JL_CALL_BIFOCAL_DECODE_PAGED ? ptr() : nullptr;
+  const int32_t *table = (const int32_t *)ptr();
+  const int64_t stride = word();
+  const int32_t cols = i32();
+  const int32_t *lens = (const int32_t *)ptr();
+  if (call == JL_CALL_BIFOCAL_SELECT_PAGES) {
+    const int32_t batch = i32(), hq = i32(), hkv = i32(), d = i32(), page = i32(), n = i32(), n_select = i32(),
+                  n_first = i32(), n_last = i32();
+    const int64_t w_pre = word();
+    const int32_t w0 = i32();
+    const double theta = f64();
+    int32_t *list = (int32_t *)ptr();
+    void *ws = ptr();
+    const size_t ws_bytes = (size_t)word();
+    const int32_t dtype = i32();
+    const uint32_t flags = u32();
+    void *stream = ptr();
+    if (!fits) return fail(JL_ERR_INVALID_ARG, "%s", kRange);
+    return jl_bifocal_select_pages(q, k, table, stride, cols, lens, batch, hq, hkv, d, page, n, n_select, n_first,
+                                   n_last, w_pre, w0, theta, list, ws, ws_bytes, (jl_dtype)dtype, flags, stream);
+  }
+  const int32_t *list = (const int32_t *)ptr();
+  const int32_t n_list = i32(), batch = i32(), hq = i32(), hkv = i32(), d = i32(), page = i32(), n = i32();
+  const int64_t page_stride = word(), w_pre = word();
+  const int32_t w0 = i32(), window = i32();
+  const double theta = f64();
+  void *out = ptr();
+  float *lse = (float *)ptr();
+  void *ws = ptr();
+  const size_t ws_bytes = (size_t)word();
+  const int32_t dtype = i32();
+  const uint32_t flags = u32();
+  void *stream = ptr();
+  if (!fits) return fail(JL_ERR_INVALID_ARG, "%s", kRange);
+  return jl_bifocal_decode_paged(q, k, v, table, stride, cols, lens, list, n_list, batch, hq, hkv, d, page, n,
+                                 page_stride, w_pre, w0, window, theta, out, lse, ws, ws_bytes, (jl_dtype)dtype, flags,
+                                 stream);
+}
+
 }  // extern "C"
 
 // ---------------------------------------------------------------- test hooks

@@ -9,7 +9,9 @@ fallback: if ``libjetlong.so`` is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -88,6 +90,8 @@ def lib() -> ctypes.CDLL:
     L.jl_bifocal_decode_paged.argtypes = ([c_p] * 4 + [c_i64, c_i32, c_p, c_p] + [c_i32] * 7 +
                                           [c_i64, c_i64, c_i32, c_i32, c_d, c_p, c_p, c_p, c_sz, ctypes.c_int,
                                            c_u32, c_p])
+    L.jl_paged_call.restype = ctypes.c_int
+    L.jl_paged_call.argtypes = [c_i32, ctypes.c_char_p, c_i32]
     L.jl_debug_set_wait_limit.restype = ctypes.c_int
     L.jl_debug_set_wait_limit.argtypes = [ctypes.c_ulonglong]
     _lib = L
@@ -270,6 +274,23 @@ def jl_bifocal_decode_noalloc_error(stream=None) -> int:
 # looked at in detail.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _device():
+    if _raw_device is not None and torch.cuda.is_initialized():
+        return _raw_device()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+# the argument words of jl_paged_call; the packed form costs a fifth of a
+# foreign call with as many arguments
+_APPEND = struct.Struct("=21qd3q")
+_SELECT = struct.Struct("=17qd6q")
+_DECODE = struct.Struct("=19qd7q")
+
+
+def _paged_call(call, words):
+    _check(lib().jl_paged_call(call, words, len(words) // 8))
 
 
 def _fits(t, shape, dtype, index):
@@ -344,9 +365,9 @@ def _heads3(name, t):
 def _scratch(workspace, nbytes, like):
     """(tensor, pointer, bytes) of the workspace; the tensor keeps it alive."""
     if nbytes == 0:
-        return None, None, 0
+        return None, 0, 0
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        workspace = like.new_empty(nbytes, dtype=torch.uint8)
         return workspace, workspace.data_ptr(), nbytes
     if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
@@ -355,16 +376,21 @@ def _scratch(workspace, nbytes, like):
 
 def _elsewhere(t, stream):
     """The context that makes t's device, and ``stream`` if there is one,
-    current; None where they are already."""
+    current; None where they are already (or t is no CUDA tensor)."""
+    if stream is None and t.get_device() == _device():
+        return None
+    if not t.is_cuda:
+        return None
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _no_host_tensor(t):
     if not t.is_cuda:
         raise ValueError(f"tensors must be on a CUDA device (got {t.device})")
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, tensors on {t.device}")
-        return torch.cuda.stream(stream)
-    if t.get_device() != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return None
 
 
 def _stream_of(t):
@@ -382,7 +408,7 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
     are rotated by their positions; without it k is stored as given.
     ``page_summary`` [n_pages, Hkv, 2, D], if given, is kept up to date.
     Returns the rotated q (``q_out``; it may be q itself) or None."""
-    elsewhere = _elsewhere(k, stream) if k.is_cuda else None
+    elsewhere = _elsewhere(k, stream)
     if elsewhere is not None:
         with elsewhere:
             return jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, max_new, page_summary, q,
@@ -397,7 +423,7 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
     cols, table_stride = _table(block_table, B, k)
     _tensor("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, k)
     _tensor("seqlens", seqlens, (B,), torch.int32, k)
-    summary = q_in = q_to = None
+    summary = q_in = q_to = 0
     if page_summary is not None:
         _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, k)
         summary = page_summary.data_ptr()
@@ -411,19 +437,20 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
             _tensor("q_out", q_out, (T, Hq, D), dtype, k)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _elsewhere(k, None)
+    _no_host_tensor(k)
     if q is not None:
         if q_out is None:
             q_out = torch.empty_like(q)
         q_in, q_to = q.data_ptr(), q_out.data_ptr()
     theta, flags = (0.0, 0) if rope_theta is None else (rope_theta, JL_FLAG_ROTATE)
-    _check(lib().jl_paged_append(
+    _paged_call(0, _APPEND.pack(
         k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), summary, block_table.data_ptr(),
-        table_stride, cols, cu_seqlens.data_ptr(), seqlens.data_ptr(), B, T, int(max_new), Hq, Hkv, D, page, n_pages,
-        page_stride, q_in, q_to, float(theta), code, flags, _stream_of(k)))
+        table_stride, cols, cu_seqlens.data_ptr(), seqlens.data_ptr(), B, T, max_new, Hq, Hkv, D, page, n_pages,
+        page_stride, q_in, q_to, theta, code, flags, _stream_of(k)))
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def jl_bifocal_select_pages_workspace_size(batch, n_kv_heads, max_pages, n_select) -> int:
     return int(lib().jl_bifocal_select_pages_workspace_size(batch, n_kv_heads, max_pages, n_select))
 
@@ -434,7 +461,7 @@ def jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_
     first, the ``n_last`` newest and the highest scored others of every kv
     head, ascending, -1 behind the last: int32 [B, Hkv, n_select], for
     jl_bifocal_decode_paged.  q [B, Hq, D] at position seqlens[b] - 1."""
-    elsewhere = _elsewhere(q, stream) if q.is_cuda else None
+    elsewhere = _elsewhere(q, stream)
     if elsewhere is not None:
         with elsewhere:
             return jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_select, w_pretrained,
@@ -451,19 +478,18 @@ def jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_
     _tensor("seqlens", seqlens, (B,), torch.int32, q)
     if out is not None:
         _tensor("out", out, (B, Hkv, n_select), torch.int32, q)
-    _elsewhere(q, None)
-    L = lib()
+    _no_host_tensor(q)
     if out is None:
-        out = torch.empty((B, Hkv, max(n_select, 0)), dtype=torch.int32, device=q.device)
-    need = L.jl_bifocal_select_pages_workspace_size(B, Hkv, cols, n_select)
-    keep, ws, ws_bytes = _scratch(workspace, need, q)
-    _check(L.jl_bifocal_select_pages(
+        out = q.new_empty((B, Hkv, max(n_select, 0)), dtype=torch.int32)
+    keep, ws, ws_bytes = _scratch(workspace, jl_bifocal_select_pages_workspace_size(B, Hkv, cols, n_select), q)
+    _paged_call(1, _SELECT.pack(
         q.data_ptr(), page_summary.data_ptr(), block_table.data_ptr(), table_stride, cols, seqlens.data_ptr(),
-        B, Hq, Hkv, D, int(page_size), n_pages, n_select, int(n_first), int(n_last), int(w_pretrained), int(w0),
-        float(rope_theta), out.data_ptr(), ws, ws_bytes, code, int(flags), _stream_of(q)))
+        B, Hq, Hkv, D, page_size, n_pages, n_select, n_first, n_last, w_pretrained, w0, rope_theta, out.data_ptr(), ws,
+        ws_bytes, code, flags, _stream_of(q)))
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def jl_bifocal_decode_paged_workspace_size(batch, head_dim) -> int:
     return int(lib().jl_bifocal_decode_paged_workspace_size(batch, head_dim))
 
@@ -474,7 +500,7 @@ def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrai
     seqlens[b] - 1 against the pages of block_table [B, max_pages]; only those
     of ``page_list`` [B, Hkv, n] if given, only the last ``window`` keys if
     not 0.  Returns (out [B, Hq, D], lse [B, Hq] or None)."""
-    elsewhere = _elsewhere(q, stream) if q.is_cuda else None
+    elsewhere = _elsewhere(q, stream)
     if elsewhere is not None:
         with elsewhere:
             return jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrained, w0, rope_theta,
@@ -489,25 +515,24 @@ def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrai
     page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, q)
     cols, table_stride = _table(block_table, B, q)
     _tensor("seqlens", seqlens, (B,), torch.int32, q)
-    listed, n_list = None, 0
+    listed, n_list = 0, 0
     if page_list is not None:
         n_list = page_list.shape[-1] if page_list.dim() == 3 else 0
         _tensor("page_list", page_list, (B, Hkv, n_list), torch.int32, q)
         # an empty list's own pointer may be null: nothing of it is read
         listed = page_list.data_ptr() or block_table.data_ptr()
-    lse_to = None
+    lse_to = 0
     if lse is not None:
         _tensor("lse", lse, (B, Hq), torch.float32, q)
         lse_to = lse.data_ptr()
     if out is not None:
         _tensor("out", out, shape, dtype, q)
-    _elsewhere(q, None)
-    L = lib()
+    _no_host_tensor(q)
     if out is None:
         out = torch.empty_like(q)
-    keep, ws, ws_bytes = _scratch(workspace, L.jl_bifocal_decode_paged_workspace_size(B, D), q)
-    _check(L.jl_bifocal_decode_paged(
+    keep, ws, ws_bytes = _scratch(workspace, jl_bifocal_decode_paged_workspace_size(B, D), q)
+    _paged_call(2, _DECODE.pack(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), table_stride, cols,
-        seqlens.data_ptr(), listed, n_list, B, Hq, Hkv, D, page, n_pages, page_stride, int(w_pretrained), int(w0),
-        int(window), float(rope_theta), out.data_ptr(), lse_to, ws, ws_bytes, code, int(flags), _stream_of(q)))
+        seqlens.data_ptr(), listed, n_list, B, Hq, Hkv, D, page, n_pages, page_stride, w_pretrained, w0, window,
+        rope_theta, out.data_ptr(), lse_to, ws, ws_bytes, code, flags, _stream_of(q)))
     return out, lse
