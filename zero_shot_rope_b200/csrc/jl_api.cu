@@ -381,7 +381,7 @@ jl_status jl_paged_append(const void *k, const void *v, void *k_pages, void *v_p
   a.GS = n_q_heads / n_kv_heads;
   a.page_stride = page_stride;
   const cudaError_t e = jl::launch_paged_append(dtype == JL_BF16, head_dim, rotate, a,
-                                                freqs_of(head_dim, rotate ? rope_theta : 1.0).inv, batch, (cudaStream_t)stream);
+                                                freqs_of(head_dim, rotate ? rope_theta : 1.0).turn, batch, (cudaStream_t)stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "paged append launch");
 }
 

@@ -296,8 +296,8 @@ struct PagedAppendArgs {
   int max_pages, page_log2, n_pages, T, max_new, Hkv, GS;
   long long page_stride;
 };
-cudaError_t launch_paged_append(bool bf16, int D, bool rotate, const PagedAppendArgs &a, const InvFreq &inv, int batch,
-                                cudaStream_t st);
+cudaError_t launch_paged_append(bool bf16, int D, bool rotate, const PagedAppendArgs &a, const TurnFreq &turn,
+                                int batch, cudaStream_t st);
 
 // ------------------------------------------------------------------ select
 struct PagedSelectArgs {

@@ -5,14 +5,15 @@
 //
 // Token at position p, pair (x_k, x_{k + D/2}), angle a = p theta^(-2k/D):
 //   (x_k cos a - x_{k+D/2} sin a,  x_{k+D/2} cos a + x_k sin a)
-// in fp32 from angles formed in 64 bits, rounded once to the cache's type.
+// in fp32, the angle as a 64-bit fraction of a turn, rounded once to the cache's
+// type.
 #include "jl_paged.cuh"
 
 namespace jl {
 
 namespace pga {
 
-constexpr int NT = 128;
+constexpr int NT = 256;
 constexpr int CHUNK = 64;  // tokens whose angles are held at a time
 
 template <typename T>
@@ -20,48 +21,56 @@ struct Vec;  // 16 bytes of a row
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const float *p, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  static __device__ __forceinline__ void unpack(uint4 v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
-  static __device__ __forceinline__ void store(float *p, const float (&x)[4]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
 };
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  static __device__ __forceinline__ void unpack(uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[2 * e] = __uint_as_float(w[e] << 16);
       x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
       w[e] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
-// CTA (page of the sequence's new tokens, kv head, sequence): that page's new
-// tokens for one kv head and its query heads, so a page's range is reduced by
-// one CTA, without atomics.  Thread: 16 bytes of the first half of a row and
-// the partner 16 bytes of the second, tokens tl, tl + TL, ...
+// CTA (page of the sequence's new tokens, up to 8 kv heads, sequence): a page's
+// new tokens, so that its ranges are reduced by one CTA, without atomics, and
+// its angles are formed once for all heads.  Keys and values: a thread has 16
+// bytes of the first half of a row and the partner 16 bytes of the second, of
+// one head, for every TL-th token, and keeps their range in registers.  A token's
+// heads lie side by side, so a warp's accesses do too.  Queries: the same 16 +
+// 16 bytes of any (token, head).  Each thread has UNROLL rows under way at once:
+// the kernel does little but move them.
+constexpr int HEADS = 8;
+constexpr int UNROLL = 4;
+
 template <typename T, int D, bool ROT>
 __global__ void __launch_bounds__(NT)
-paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_constant__ InvFreq inv) {
-  constexpr int N = Vec<T>::N, HALF = D / 2, CT = HALF / N, TL = NT / CT;
-  __shared__ float2 cs[ROT ? CHUNK : 1][HALF];
-  __shared__ float red[2][NT / 32][D];
-  const int b = blockIdx.z, kvh = blockIdx.y;
+paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_constant__ TurnFreq turn) {
+  constexpr int N = Vec<T>::N, HALF = D / 2, CT = HALF / N;
+  // the angles of CHUNK tokens (two neighbouring pairs: cos, cos, sin, sin), then the threads' ranges
+  constexpr int ANG = ROT ? CHUNK * HALF * 8 : 0, RED = NT * 4 * N * 4;
+  __shared__ __align__(16) uint8_t smem[ANG > RED ? ANG : RED];
+  float4(*cs)[HALF / 2] = reinterpret_cast<float4(*)[HALF / 2]>(smem);
+  float(*red)[NT] = reinterpret_cast<float(*)[NT]>(smem);
+  const int b = blockIdx.z, h0 = blockIdx.y * HEADS, heads = min(HEADS, a.Hkv - h0);
   let_next_kernel_come();
   wait_for_kernel_before();
   const int c0 = a.cu[b], n = a.cu[b + 1] - c0, L = a.seqlens[b];
@@ -74,131 +83,151 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
   const int ja = (int)max(pb, (long long)(L - n)), je = (int)min(pb + P, (long long)L);  // this page's new tokens
   int page = lp < a.max_pages ? a.table[(long long)b * a.table_stride + lp] : -1;
   if (page >= a.n_pages) page = -1;  // no such page: only the queries are written
-  const int tl = threadIdx.x / CT, ch = threadIdx.x % CT;
-  const int Hq = a.Hkv * a.GS;
+  const int cols = heads * CT, TL = NT / cols;
+  const int col = threadIdx.x % cols, tl = threadIdx.x / cols;  // (threads past cols TL have no keys)
+  const int ch = col % CT;
   float lo[2][N], hi[2][N];
 #pragma unroll
   for (int e = 0; e < N; ++e) lo[0][e] = lo[1][e] = INFINITY, hi[0][e] = hi[1][e] = -INFINITY;
+  auto rotate = [&](int x, int chunk, float (&u)[N], float (&v)[N]) {
+    if constexpr (ROT) {
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        const float4 f = cs[x][(chunk * N + e) / 2];
+        float t = fmaf(u[e], f.x, -(v[e] * f.z));
+        v[e] = fmaf(v[e], f.x, u[e] * f.z);
+        u[e] = t;
+        t = fmaf(u[e + 1], f.y, -(v[e + 1] * f.w));
+        v[e + 1] = fmaf(v[e + 1], f.y, u[e + 1] * f.w);
+        u[e + 1] = t;
+      }
+    }
+  };
 
   for (int j0 = ja; j0 < je; j0 += CHUNK) {
     const int m = min(CHUNK, je - j0);
+    const size_t tok0 = (size_t)c0 + (size_t)(j0 - (L - n));
     if constexpr (ROT) {
-      // thread: one pair's angles of a run of tokens; the first in 64 bits,
-      // the next by 64-bit steps of one position
-      constexpr int RUNS = NT / HALF;
-      const int k = threadIdx.x % HALF, r = threadIdx.x / HALF;
-      const int per = (m + RUNS - 1) / RUNS, x0 = r * per, x1 = min(m, x0 + per);
       __syncthreads();
-      if (x0 < x1) {
-        double c, s, c1, s1;
-        sincos_fp64((double)(j0 + x0) * inv.v[k], s, c);
-        sincos_fp64(inv.v[k], s1, c1);
-        for (int x = x0; x < x1; ++x) {
-          cs[x][k] = make_float2((float)c, (float)s);
-          const double cn = c * c1 - s * s1;
-          s = s * c1 + c * s1;
-          c = cn;
-        }
+      for (int idx = threadIdx.x; idx < m * HALF; idx += NT) {
+        const int x = idx / HALF, k = idx % HALF;
+        float c, s;
+        turn_cs(j0 + x, turn.v[k], c, s);
+        float *to = reinterpret_cast<float *>(&cs[x][k / 2]) + (k & 1);
+        to[0] = c;
+        to[2] = s;
       }
       __syncthreads();
     }
-    for (int x = tl; x < m; x += TL) {
-      const int j = j0 + x;
-      const size_t tok = (size_t)c0 + (size_t)(j - (L - n));
-      float co[N], si[N];
-      if constexpr (ROT) {
+    if (page >= 0 && tl < TL) {
+      const size_t from = (tok0 * a.Hkv + h0) * D + (size_t)(col / CT) * D + ch * N, step = (size_t)a.Hkv * D;
+      const size_t to = (size_t)page * a.page_stride + ((size_t)(j0 & (P - 1)) * a.Hkv + h0) * D +
+                        (size_t)(col / CT) * D + ch * N;
+      for (int x0 = tl; x0 < m; x0 += TL * UNROLL) {
+        uint4 ka[UNROLL], kb[UNROLL], va[UNROLL], vb[UNROLL];
 #pragma unroll
-        for (int e = 0; e < N; ++e) co[e] = cs[x][ch * N + e].x, si[e] = cs[x][ch * N + e].y;
-      }
-      auto turn = [&](float (&u)[N], float (&v)[N]) {
-        if constexpr (ROT) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const float t = fmaf(u[e], co[e], -(v[e] * si[e]));
-            v[e] = fmaf(v[e], co[e], u[e] * si[e]);
-            u[e] = t;
+        for (int y = 0; y < UNROLL; ++y) {
+          const size_t at = from + (size_t)(x0 + y * TL) * step;
+          if (x0 + y * TL < m) {
+            ka[y] = *reinterpret_cast<const uint4 *>((const T *)a.k + at);
+            kb[y] = *reinterpret_cast<const uint4 *>((const T *)a.k + at + HALF);
+            va[y] = *reinterpret_cast<const uint4 *>((const T *)a.v + at);
+            vb[y] = *reinterpret_cast<const uint4 *>((const T *)a.v + at + HALF);
           }
         }
-      };
-      if (page >= 0) {
-        const size_t src = (tok * a.Hkv + kvh) * D + ch * N;
-        const size_t dst = (size_t)page * a.page_stride + ((size_t)(j & (P - 1)) * a.Hkv + kvh) * D + ch * N;
-        float u[N], v[N];
-        Vec<T>::load((const T *)a.k + src, u);
-        Vec<T>::load((const T *)a.k + src + HALF, v);
-        turn(u, v);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {  // the range is that of the stored values
-          u[e] = to_f(from_f<T>(u[e]));
-          v[e] = to_f(from_f<T>(v[e]));
-          lo[0][e] = min_nan(lo[0][e], u[e]), hi[0][e] = max_nan(hi[0][e], u[e]);
-          lo[1][e] = min_nan(lo[1][e], v[e]), hi[1][e] = max_nan(hi[1][e], v[e]);
-        }
-        Vec<T>::store((T *)a.k_pages + dst, u);
-        Vec<T>::store((T *)a.k_pages + dst + HALF, v);
-        *reinterpret_cast<uint4 *>((T *)a.v_pages + dst) = *reinterpret_cast<const uint4 *>((const T *)a.v + src);
-        *reinterpret_cast<uint4 *>((T *)a.v_pages + dst + HALF) =
-            *reinterpret_cast<const uint4 *>((const T *)a.v + src + HALF);
-      }
-      if (ROT && a.q != nullptr) {
-        for (int g = 0; g < a.GS; ++g) {
-          const size_t at = (tok * Hq + (size_t)kvh * a.GS + g) * D + ch * N;
+        for (int y = 0; y < UNROLL; ++y) {
+          const int x = x0 + y * TL;
+          if (x >= m) break;
+          const size_t at = to + (size_t)x * step;
+          *reinterpret_cast<uint4 *>((T *)a.v_pages + at) = va[y];
+          *reinterpret_cast<uint4 *>((T *)a.v_pages + at + HALF) = vb[y];
           float u[N], v[N];
-          Vec<T>::load((const T *)a.q + at, u);
-          Vec<T>::load((const T *)a.q + at + HALF, v);
-          turn(u, v);
-          Vec<T>::store((T *)a.q_out + at, u);
-          Vec<T>::store((T *)a.q_out + at + HALF, v);
+          Vec<T>::unpack(ka[y], u);
+          Vec<T>::unpack(kb[y], v);
+          rotate(x, ch, u, v);
+          const uint4 pu = Vec<T>::pack(u), pv = Vec<T>::pack(v);
+          *reinterpret_cast<uint4 *>((T *)a.k_pages + at) = pu;
+          *reinterpret_cast<uint4 *>((T *)a.k_pages + at + HALF) = pv;
+          Vec<T>::unpack(pu, u);  // the range is that of the stored values
+          Vec<T>::unpack(pv, v);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            lo[0][e] = min_nan(lo[0][e], u[e]), hi[0][e] = max_nan(hi[0][e], u[e]);
+            lo[1][e] = min_nan(lo[1][e], v[e]), hi[1][e] = max_nan(hi[1][e], v[e]);
+          }
+        }
+      }
+    }
+    if (ROT && a.q != nullptr) {
+      // pieces of a token's heads; a thread has one (or every NT-th) of every QL-th token
+      const int row = heads * a.GS * CT, wide = min(row, NT), QL = NT / wide, ql = threadIdx.x / wide;
+      const size_t step = (size_t)a.Hkv * a.GS * D;
+      for (int i = threadIdx.x % wide; ql < QL && i < row; i += wide) {
+        const size_t from = tok0 * step + ((size_t)h0 * a.GS + i / CT) * D + i % CT * N;
+        for (int x0 = ql; x0 < m; x0 += QL * UNROLL) {
+          uint4 qa[UNROLL], qb[UNROLL];
+#pragma unroll
+          for (int y = 0; y < UNROLL; ++y)
+            if (x0 + y * QL < m) {
+              qa[y] = *reinterpret_cast<const uint4 *>((const T *)a.q + from + (size_t)(x0 + y * QL) * step);
+              qb[y] = *reinterpret_cast<const uint4 *>((const T *)a.q + from + (size_t)(x0 + y * QL) * step + HALF);
+            }
+#pragma unroll
+          for (int y = 0; y < UNROLL; ++y) {
+            const int x = x0 + y * QL;
+            if (x >= m) break;
+            float u[N], v[N];
+            Vec<T>::unpack(qa[y], u);
+            Vec<T>::unpack(qb[y], v);
+            rotate(x, i % CT, u, v);
+            *reinterpret_cast<uint4 *>((T *)a.q_out + from + (size_t)x * step) = Vec<T>::pack(u);
+            *reinterpret_cast<uint4 *>((T *)a.q_out + from + (size_t)x * step + HALF) = Vec<T>::pack(v);
+          }
         }
       }
     }
   }
 
   if (a.summary == nullptr || page < 0) return;  // uniform over the CTA
-  // lanes of a warp with the same chunk, then the warps
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
+  __syncthreads();
+  const int live = min(TL, je - ja);  // token lanes that had one
+  if (tl < live) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-#pragma unroll
-      for (int o = CT; o < 32; o <<= 1) {
-        lo[h][e] = min_nan(lo[h][e], __shfl_xor_sync(0xffffffffu, lo[h][e], o));
-        hi[h][e] = max_nan(hi[h][e], __shfl_xor_sync(0xffffffffu, hi[h][e], o));
-      }
-      if ((threadIdx.x & 31) < CT) {
-        red[0][threadIdx.x >> 5][h * HALF + ch * N + e] = lo[h][e];
-        red[1][threadIdx.x >> 5][h * HALF + ch * N + e] = hi[h][e];
-      }
+      red[e][threadIdx.x] = lo[0][e], red[N + e][threadIdx.x] = lo[1][e];
+      red[2 * N + e][threadIdx.x] = hi[0][e], red[3 * N + e][threadIdx.x] = hi[1][e];
     }
+  }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < 2 * D; idx += NT) {
-    const int side = idx / D, d = idx % D;
-    float x = red[side][0][d];
-#pragma unroll
-    for (int w = 1; w < NT / 32; ++w) x = side == 0 ? min_nan(x, red[0][w][d]) : max_nan(x, red[1][w][d]);
-    T *to = (T *)a.summary + (((size_t)page * a.Hkv + kvh) * 2 + side) * D + d;
+  for (int idx = threadIdx.x; idx < heads * 2 * D; idx += NT) {
+    const int h = idx / (2 * D), side = idx / D % 2, d = idx % D;
+    const int slot = side * 2 * N + d / HALF * N + d % N, at = h * CT + d % HALF / N;
+    float x = red[slot][at];
+    for (int y = 1; y < live; ++y) x = side == 0 ? min_nan(x, red[slot][at + y * cols]) : max_nan(x, red[slot][at + y * cols]);
+    T *to = (T *)a.summary + (((size_t)page * a.Hkv + h0 + h) * 2 + side) * D + d;
     if (ja > pb) x = side == 0 ? min_nan(x, to_f(*to)) : max_nan(x, to_f(*to));  // the page had tokens before
     *to = from_f<T>(x);
   }
 }
 
 template <typename T, int D>
-cudaError_t launch(bool rotate, const PagedAppendArgs &a, const InvFreq &inv, int batch, cudaStream_t st) {
+cudaError_t launch(bool rotate, const PagedAppendArgs &a, const TurnFreq &turn, int batch, cudaStream_t st) {
   const int P = 1 << a.page_log2;
-  const dim3 grid((unsigned)(((long long)a.max_new + 2 * P - 2) / P), a.Hkv, batch);
+  const dim3 grid((unsigned)(((long long)a.max_new + 2 * P - 2) / P), (a.Hkv + HEADS - 1) / HEADS, batch);
   const auto kernel = rotate ? paged_append_kernel<T, D, true> : paged_append_kernel<T, D, false>;
-  return launch_overlapped(kernel, grid, NT, 0, st, a, inv);
+  return launch_overlapped(kernel, grid, NT, 0, st, a, turn);
 }
 
 }  // namespace pga
 
-cudaError_t launch_paged_append(bool bf16, int D, bool rotate, const PagedAppendArgs &a, const InvFreq &inv, int batch,
-                                cudaStream_t st) {
+cudaError_t launch_paged_append(bool bf16, int D, bool rotate, const PagedAppendArgs &a, const TurnFreq &turn,
+                                int batch, cudaStream_t st) {
   if (D == 128)
-    return bf16 ? pga::launch<__nv_bfloat16, 128>(rotate, a, inv, batch, st)
-                : pga::launch<float, 128>(rotate, a, inv, batch, st);
-  return bf16 ? pga::launch<__nv_bfloat16, 64>(rotate, a, inv, batch, st)
-              : pga::launch<float, 64>(rotate, a, inv, batch, st);
+    return bf16 ? pga::launch<__nv_bfloat16, 128>(rotate, a, turn, batch, st)
+                : pga::launch<float, 128>(rotate, a, turn, batch, st);
+  return bf16 ? pga::launch<__nv_bfloat16, 64>(rotate, a, turn, batch, st)
+              : pga::launch<float, 64>(rotate, a, turn, batch, st);
 }
 
 }  // namespace jl
