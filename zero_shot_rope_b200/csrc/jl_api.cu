@@ -512,8 +512,8 @@ jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void
   a.tab = (long long *)((char *)a.part_ml + align256(rows * 2 * sizeof(float)));
   a.out = out;
   a.lse = lse;
-  const Freqs &f = freqs_of(head_dim, rope_theta);
-  const cudaError_t e = jl::launch_paged_decode(dtype == JL_BF16, head_dim, a, f.inv, f.turn, (cudaStream_t)stream);
+  const cudaError_t e =
+      jl::launch_paged_decode(dtype == JL_BF16, head_dim, a, freqs_of(head_dim, rope_theta).turn, (cudaStream_t)stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "paged decode launch");
 }
 

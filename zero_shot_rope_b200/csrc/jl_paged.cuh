@@ -284,7 +284,7 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
 // The tensor-core kernel (bf16): the partial results only; paged_decode_tc_ctas() runs.
 int paged_decode_tc_ctas();
 cudaError_t launch_paged_decode_tc(int D, const PagedDecodeArgs &a, const TurnFreq &turn, cudaStream_t st);
-cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, const TurnFreq &turn, cudaStream_t st);
+cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const TurnFreq &turn, cudaStream_t st);
 
 // ------------------------------------------------------------------ append
 struct PagedAppendArgs {

@@ -56,13 +56,15 @@ struct Vec<__nv_bfloat16> {
 // bytes of the first half of a row and the partner 16 bytes of the second, of
 // one head, for every TL-th token, and keeps their range in registers.  A token's
 // heads lie side by side, so a warp's accesses do too.  Queries: the same 16 +
-// 16 bytes of any (token, head).  Each thread has UNROLL rows under way at once:
-// the kernel does little but move them.
+// 16 bytes of any (token, head).  The kernel does little but move rows, so a
+// thread asks for its next UNROLL rows before it works on the last ones, and two
+// CTAs share an SM: 32K tokens of 16/8 heads in 106 us, 5.1 TB/s, where a plain
+// copy of as many bytes takes 89 us.
 constexpr int HEADS = 8;
-constexpr int UNROLL = 4;
+constexpr int UNROLL = 2;
 
 template <typename T, int D, bool ROT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 2)
 paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_constant__ TurnFreq turn) {
   constexpr int N = Vec<T>::N, HALF = D / 2, CT = HALF / N;
   // the angles of CHUNK tokens (two neighbouring pairs: cos, cos, sin, sin), then the threads' ranges
@@ -123,28 +125,30 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
       const size_t from = (tok0 * a.Hkv + h0) * D + (size_t)(col / CT) * D + ch * N, step = (size_t)a.Hkv * D;
       const size_t to = (size_t)page * a.page_stride + ((size_t)(j0 & (P - 1)) * a.Hkv + h0) * D +
                         (size_t)(col / CT) * D + ch * N;
-      for (int x0 = tl; x0 < m; x0 += TL * UNROLL) {
-        uint4 ka[UNROLL], kb[UNROLL], va[UNROLL], vb[UNROLL];
+      uint4 buf[2][UNROLL / 2][4];
+      auto load = [&](uint4 (&r)[UNROLL / 2][4], int x0) {
 #pragma unroll
-        for (int y = 0; y < UNROLL; ++y) {
+        for (int y = 0; y < UNROLL / 2; ++y) {
           const size_t at = from + (size_t)(x0 + y * TL) * step;
           if (x0 + y * TL < m) {
-            ka[y] = *reinterpret_cast<const uint4 *>((const T *)a.k + at);
-            kb[y] = *reinterpret_cast<const uint4 *>((const T *)a.k + at + HALF);
-            va[y] = *reinterpret_cast<const uint4 *>((const T *)a.v + at);
-            vb[y] = *reinterpret_cast<const uint4 *>((const T *)a.v + at + HALF);
+            r[y][0] = *reinterpret_cast<const uint4 *>((const T *)a.k + at);
+            r[y][1] = *reinterpret_cast<const uint4 *>((const T *)a.k + at + HALF);
+            r[y][2] = *reinterpret_cast<const uint4 *>((const T *)a.v + at);
+            r[y][3] = *reinterpret_cast<const uint4 *>((const T *)a.v + at + HALF);
           }
         }
+      };
+      auto use = [&](const uint4 (&r)[UNROLL / 2][4], int x0) {
 #pragma unroll
-        for (int y = 0; y < UNROLL; ++y) {
+        for (int y = 0; y < UNROLL / 2; ++y) {
           const int x = x0 + y * TL;
           if (x >= m) break;
           const size_t at = to + (size_t)x * step;
-          *reinterpret_cast<uint4 *>((T *)a.v_pages + at) = va[y];
-          *reinterpret_cast<uint4 *>((T *)a.v_pages + at + HALF) = vb[y];
+          *reinterpret_cast<uint4 *>((T *)a.v_pages + at) = r[y][2];
+          *reinterpret_cast<uint4 *>((T *)a.v_pages + at + HALF) = r[y][3];
           float u[N], v[N];
-          Vec<T>::unpack(ka[y], u);
-          Vec<T>::unpack(kb[y], v);
+          Vec<T>::unpack(r[y][0], u);
+          Vec<T>::unpack(r[y][1], v);
           rotate(x, ch, u, v);
           const uint4 pu = Vec<T>::pack(u), pv = Vec<T>::pack(v);
           *reinterpret_cast<uint4 *>((T *)a.k_pages + at) = pu;
@@ -157,6 +161,14 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
             lo[1][e] = min_nan(lo[1][e], v[e]), hi[1][e] = max_nan(hi[1][e], v[e]);
           }
         }
+      };
+      const int batch = TL * UNROLL / 2;
+      load(buf[0], tl);
+      for (int x0 = tl; x0 < m; x0 += 2 * batch) {
+        load(buf[1], x0 + batch);
+        use(buf[0], x0);
+        load(buf[0], x0 + 2 * batch);
+        use(buf[1], x0 + batch);
       }
     }
     if (ROT && a.q != nullptr) {
@@ -165,25 +177,34 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
       const size_t step = (size_t)a.Hkv * a.GS * D;
       for (int i = threadIdx.x % wide; ql < QL && i < row; i += wide) {
         const size_t from = tok0 * step + ((size_t)h0 * a.GS + i / CT) * D + i % CT * N;
-        for (int x0 = ql; x0 < m; x0 += QL * UNROLL) {
-          uint4 qa[UNROLL], qb[UNROLL];
+        uint4 buf[2][UNROLL][2];
+        auto load = [&](uint4 (&r)[UNROLL][2], int x0) {
 #pragma unroll
           for (int y = 0; y < UNROLL; ++y)
             if (x0 + y * QL < m) {
-              qa[y] = *reinterpret_cast<const uint4 *>((const T *)a.q + from + (size_t)(x0 + y * QL) * step);
-              qb[y] = *reinterpret_cast<const uint4 *>((const T *)a.q + from + (size_t)(x0 + y * QL) * step + HALF);
+              r[y][0] = *reinterpret_cast<const uint4 *>((const T *)a.q + from + (size_t)(x0 + y * QL) * step);
+              r[y][1] = *reinterpret_cast<const uint4 *>((const T *)a.q + from + (size_t)(x0 + y * QL) * step + HALF);
             }
+        };
+        auto use = [&](const uint4 (&r)[UNROLL][2], int x0) {
 #pragma unroll
           for (int y = 0; y < UNROLL; ++y) {
             const int x = x0 + y * QL;
             if (x >= m) break;
             float u[N], v[N];
-            Vec<T>::unpack(qa[y], u);
-            Vec<T>::unpack(qb[y], v);
+            Vec<T>::unpack(r[y][0], u);
+            Vec<T>::unpack(r[y][1], v);
             rotate(x, i % CT, u, v);
             *reinterpret_cast<uint4 *>((T *)a.q_out + from + (size_t)x * step) = Vec<T>::pack(u);
             *reinterpret_cast<uint4 *>((T *)a.q_out + from + (size_t)x * step + HALF) = Vec<T>::pack(v);
           }
+        };
+        load(buf[0], ql);
+        for (int x0 = ql; x0 < m; x0 += 2 * QL * UNROLL) {
+          load(buf[1], x0 + QL * UNROLL);
+          use(buf[0], x0);
+          load(buf[0], x0 + 2 * QL * UNROLL);
+          use(buf[1], x0 + QL * UNROLL);
         }
       }
     }

@@ -1,5 +1,5 @@
-// Decode of one new token per sequence over a paged cache (sm_100a): the
-// CUDA-core kernel and the combine.
+// Decode of one new token per sequence over a paged cache (sm_100a): the fp32
+// kernel and the combine.
 //
 // The attention is jl_bifocal_decode's: with i = L - 1, G = G(L) and
 // n(p) = p - floor(p / G), key j is scored as
@@ -20,43 +20,51 @@ constexpr float LOG2E_F = 1.4426950408889634f;
 
 // PPL rotation pairs per lane: lane l holds elements PPL l .. PPL l + PPL - 1 of the
 // first half of a row and the same of the second
-template <typename T, int PPL>
-__device__ __forceinline__ void load_pairs(const T *row, int half, int lane, float (&a)[PPL], float (&b)[PPL]) {
-  if constexpr (PPL == 2 && sizeof(T) == 4) {
+template <int PPL>
+__device__ __forceinline__ void load_pairs(const float *row, int half, int lane, float (&a)[PPL], float (&b)[PPL]) {
+  if constexpr (PPL == 2) {
     const float2 x = *reinterpret_cast<const float2 *>(row + 2 * lane);
     const float2 y = *reinterpret_cast<const float2 *>(row + half + 2 * lane);
     a[0] = x.x, a[1] = x.y, b[0] = y.x, b[1] = y.y;
-  } else if constexpr (PPL == 2) {
-    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(row + 2 * lane));
-    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(row + half + 2 * lane));
-    a[0] = x.x, a[1] = x.y, b[0] = y.x, b[1] = y.y;
   } else {
-    a[0] = to_f(row[lane]);
-    b[0] = to_f(row[half + lane]);
+    a[0] = row[lane];
+    b[0] = row[half + lane];
   }
 }
 
 // One warp takes 8 keys (half a 16-key block) of every tile and keeps its own
 // running maximum, sum and output; the warps are merged when the CTA leaves a
-// (sequence, kv head, head block).
-template <typename T, int D, int GP>
-__global__ void __launch_bounds__(NT)
-paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_constant__ InvFreq inv) {
+// (sequence, kv head, head block).  The cache is read once, straight into
+// registers: a lane has four channels (two at head_dim 64) of all eight keys.
+// The 8 keys x 4 heads partial scores are added up over the lanes together (with
+// each shuffle a lane hands over half of what it holds), which leaves one whole
+// score in each lane: every exponential is taken once.  The weights go through
+// shared memory to all lanes.  Four heads at a time bound the registers.
+constexpr int ctas_per_sm(int gp) { return gp <= 4 ? 2 : 1; }  // by their registers
+
+template <int D, int GP>
+__global__ void __launch_bounds__(NT, ctas_per_sm(GP))
+paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_constant__ TurnFreq turn) {
   constexpr int PPL = D / 64, HALF = D / 2, KW = 8;
+  constexpr int GC = GP < 4 ? GP : 4, NC = GP / GC;  // heads at a time, and how often
+  constexpr int NV = KW * GC;                        // their scores: NV lanes (and copies)
   __shared__ float red_ml[NW][GP][2];
   __shared__ float red_o[NW][GP][D];
+  __shared__ __align__(16) float w_s[NW][KW][GC], f_s[NW][GC];
   let_next_kernel_come();
   wait_for_kernel_before();
   const PagedRun run = paged_plan<NT>(p);
   if (threadIdx.x == 0) p.cta_err[blockIdx.x] = 0;  // this kernel has no waits that could run out
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float scale = rsqrtf((float)D) * LOG2E_F;
-  double w[PPL];
+  // this lane's score: key lk, head lg of the four
+  const int lk = lane / (32 / KW), lg = lane / (32 / NV) % GC;
+  unsigned long long w[PPL];
   float c1[PPL], s1[PPL];  // rotation by one position
 #pragma unroll
   for (int e = 0; e < PPL; ++e) {
-    w[e] = inv.v[PPL * lane + e];
-    angle_cs(1, w[e], c1[e], s1[e]);
+    w[e] = turn.v[PPL * lane + e];
+    turn_cs(1, w[e], c1[e], s1[e]);
   }
 
   PagedWalk walk(p, run);
@@ -66,51 +74,55 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
     const int kvh = pair / p.HB, hb = pair % p.HB;
     const int gh = min(PD_HEADS, p.GS - hb * PD_HEADS);
     const int h0 = kvh * p.GS + hb * PD_HEADS;  // first query head
-    const int i = s.L - 1;
     const int G = p.plain ? 1 : (int)group_size(s.L, p.w_pre);
-    const int ni = corr_n(i, G);
+    const int ni = corr_n(s.L - 1, G);
     const int j_local = (int)max(0LL, (long long)s.L - (long long)p.w0);
 
-    float qa[GP][PPL], qb[GP][PPL], oa[GP][PPL], ob[GP][PPL], m[GP], l[GP];
+    float qa[GP][PPL], qb[GP][PPL], oa[GP][PPL], ob[GP][PPL];
+    float m[NC], l[NC];  // of head lg (+ 4): maximum, and this lane's part of the sum
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
-      m[g] = -INFINITY;
-      l[g] = 0.f;
 #pragma unroll
       for (int e = 0; e < PPL; ++e) qa[g][e] = qb[g][e] = oa[g][e] = ob[g][e] = 0.f;
       if (g < gh) {
-        load_pairs<T, PPL>((const T *)p.q + ((size_t)b * p.Hq + h0 + g) * D, HALF, lane, qa[g], qb[g]);
+        load_pairs<PPL>((const float *)p.q + ((size_t)b * p.Hq + h0 + g) * D, HALF, lane, qa[g], qb[g]);
 #pragma unroll
         for (int e = 0; e < PPL; ++e) qa[g][e] *= scale, qb[g][e] *= scale;
       }
     }
+#pragma unroll
+    for (int x = 0; x < NC; ++x) m[x] = -INFINITY, l[x] = 0.f;
 
+    int page = 0, jb = paged_block(p, s, b, kvh, u0, warp >> 1, page);
     for (int u = u0; u < u1; ++u) {
-      int page;
-      const int jb = paged_block(p, s, b, kvh, u, warp >> 1, page);
-      if (jb < 0) continue;
       const int j0 = jb + (warp & 1) * KW;
-      if (j0 >= s.L || j0 + KW <= s.jw) continue;
-      const size_t row0 = (size_t)page * p.page_stride +
-                          ((size_t)(j0 & ((1 << p.page_log2) - 1)) * p.Hkv + kvh) * D;
+      const bool some = jb >= 0 && j0 < s.L && j0 + KW > s.jw;
       float ka[KW][PPL], kb[KW][PPL], va[KW][PPL], vb[KW][PPL];
+      if (some) {
+        const size_t row0 = (size_t)page * p.page_stride +
+                            ((size_t)(j0 & ((1 << p.page_log2) - 1)) * p.Hkv + kvh) * D;
 #pragma unroll
-      for (int x = 0; x < KW; ++x) {
-        if (j0 + x < s.L) {  // rows past the length may hold anything
-          load_pairs<T, PPL>((const T *)p.k + row0 + (size_t)x * p.Hkv * D, HALF, lane, ka[x], kb[x]);
-          load_pairs<T, PPL>((const T *)p.v + row0 + (size_t)x * p.Hkv * D, HALF, lane, va[x], vb[x]);
-        } else {
+        for (int x = 0; x < KW; ++x) {
+          if (j0 + x < s.L && j0 + x >= s.jw) {  // other rows may hold anything
+            load_pairs<PPL>((const float *)p.k + row0 + (size_t)x * p.Hkv * D, HALF, lane, ka[x], kb[x]);
+            load_pairs<PPL>((const float *)p.v + row0 + (size_t)x * p.Hkv * D, HALF, lane, va[x], vb[x]);
+          } else {
 #pragma unroll
-          for (int e = 0; e < PPL; ++e) ka[x][e] = kb[x][e] = va[x][e] = vb[x][e] = 0.f;
+            for (int e = 0; e < PPL; ++e) ka[x][e] = kb[x][e] = va[x][e] = vb[x][e] = 0.f;
+          }
         }
       }
+      // the next tile's page, while this tile's rows come
+      if (u + 1 < u1) jb = paged_block(p, s, b, kvh, u + 1, warp >> 1, page);
+      if (!some) continue;
       if (G > 1 && j0 < j_local) {
-        // the angle of the first key in 64 bits, the next ones a step of one
-        // position or none (j + 1 a multiple of G) further
+        // the angle of the first key, the next ones a step of one position or
+        // none (j + 1 a multiple of G) further
         float c[PPL], sn[PPL];
+        const int f = j0 / G;
+        int rho = j0 - f * G;
 #pragma unroll
-        for (int e = 0; e < PPL; ++e) angle_cs(corr_n(j0, G) - ni, w[e], c[e], sn[e]);
-        int rho = j0 % G;
+        for (int e = 0; e < PPL; ++e) turn_cs(j0 - f - ni, w[e], c[e], sn[e]);
 #pragma unroll
         for (int x = 0; x < KW; ++x) {
           if (j0 + x < j_local)
@@ -129,33 +141,73 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
         }
       }
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        float sc[KW], top = -INFINITY;
+      for (int y = 0; y < NC; ++y) {
+        float d[NV];
 #pragma unroll
-        for (int x = 0; x < KW; ++x) {
-          float d = 0.f;
+        for (int x = 0; x < KW; ++x)
 #pragma unroll
-          for (int e = 0; e < PPL; ++e) d = fmaf(qa[g][e], ka[x][e], fmaf(qb[g][e], kb[x][e], d));
-          d = warp_sum(d);
-          sc[x] = (j0 + x < s.L && j0 + x >= s.jw) ? d : -INFINITY;
-          top = max_nan(top, sc[x]);
-        }
-        const float mn = max_nan(m[g], top);
-        if (mn == -INFINITY) continue;  // every score so far is -inf
-        const float f = exp2f(m[g] - mn);
-        m[g] = mn;
-        l[g] *= f;
+          for (int g = 0; g < GC; ++g) {
+            float t = 0.f;
 #pragma unroll
-        for (int e = 0; e < PPL; ++e) oa[g][e] *= f, ob[g][e] *= f;
-#pragma unroll
-        for (int x = 0; x < KW; ++x) {
-          const float pr = exp2f(sc[x] - mn);
-          l[g] += pr;
-#pragma unroll
-          for (int e = 0; e < PPL; ++e) {
-            oa[g][e] = fmaf(pr, va[x][e], oa[g][e]);
-            ob[g][e] = fmaf(pr, vb[x][e], ob[g][e]);
+            for (int e = 0; e < PPL; ++e)
+              t = fmaf(qa[y * GC + g][e], ka[x][e], fmaf(qb[y * GC + g][e], kb[x][e], t));
+            d[x * GC + g] = t;
           }
+        int o = 16;
+#pragma unroll
+        for (int n = NV; n > 1; n >>= 1, o >>= 1)
+#pragma unroll
+          for (int i = 0; i < n / 2; ++i) {
+            const bool up = lane & o;
+            const float keep = up ? d[i + n / 2] : d[i], give = up ? d[i] : d[i + n / 2];
+            d[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        float sc = d[0];
+#pragma unroll
+        for (; o > 0; o >>= 1) sc += __shfl_xor_sync(0xffffffffu, sc, o);
+        if (j0 + lk >= s.L || j0 + lk < s.jw) sc = -INFINITY;
+        float top = sc;
+#pragma unroll
+        for (int x = 16; x >= 32 / KW; x >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, x));
+        // the maximum is only moved when it has grown by more than 2^8
+        const bool grow = !(top <= m[y] + 8.f) && !(top == -INFINITY);
+        const bool any = __any_sync(0xffffffffu, grow);
+        float f = 1.f;
+        if (grow) {
+          f = m[y] == -INFINITY ? 0.f : exp2f(m[y] - top);
+          m[y] = top;
+        }
+        const float pr = exp2f(sc - (m[y] == -INFINITY ? 0.f : m[y]));
+        l[y] = fmaf(l[y], f, pr);
+        __syncwarp();
+        w_s[warp][lk][lg] = pr;
+        if (any) f_s[warp][lg] = f;
+        __syncwarp();
+        if (any) {
+#pragma unroll
+          for (int g = 0; g < GC; ++g) {
+            const float fg = f_s[warp][g];
+#pragma unroll
+            for (int e = 0; e < PPL; ++e) oa[y * GC + g][e] *= fg, ob[y * GC + g][e] *= fg;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < KW; ++x) {
+          float pg[GC];
+          if constexpr (GC == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(w_s[warp][x]);
+            pg[0] = v.x, pg[1] = v.y, pg[2] = v.z, pg[3] = v.w;
+          } else {
+#pragma unroll
+            for (int g = 0; g < GC; ++g) pg[g] = w_s[warp][x][g];
+          }
+#pragma unroll
+          for (int g = 0; g < GC; ++g)
+#pragma unroll
+            for (int e = 0; e < PPL; ++e) {
+              oa[y * GC + g][e] = fmaf(pg[g], va[x][e], oa[y * GC + g][e]);
+              ob[y * GC + g][e] = fmaf(pg[g], vb[x][e], ob[y * GC + g][e]);
+            }
         }
       }
     }
@@ -163,14 +215,18 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
     // merge the warps
     __syncthreads();
 #pragma unroll
-    for (int g = 0; g < GP; ++g) {
-      if (lane == 0) red_ml[warp][g][0] = m[g], red_ml[warp][g][1] = l[g];
+    for (int y = 0; y < NC; ++y) {
+#pragma unroll
+      for (int x = 16; x >= 32 / KW; x >>= 1) l[y] += __shfl_xor_sync(0xffffffffu, l[y], x);
+      if (lk == 0) red_ml[warp][y * GC + lg][0] = m[y], red_ml[warp][y * GC + lg][1] = l[y];
+    }
+#pragma unroll
+    for (int g = 0; g < GP; ++g)
 #pragma unroll
       for (int e = 0; e < PPL; ++e) {
         red_o[warp][g][PPL * lane + e] = oa[g][e];
         red_o[warp][g][HALF + PPL * lane + e] = ob[g][e];
       }
-    }
     __syncthreads();
     const bool whole = u0 == 0 && u1 == s.tiles;
     const size_t slot = 2 * (size_t)blockIdx.x + (u0 > 0 ? 0 : 1);
@@ -186,7 +242,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
         }
       if (whole) {
         const size_t bh = (size_t)b * p.Hq + h0 + g;
-        ((T *)p.out)[bh * D + d] = from_f<T>(M != -INFINITY ? acc / L : 0.f);
+        ((float *)p.out)[bh * D + d] = M != -INFINITY ? acc / L : 0.f;
         if (p.lse != nullptr && d == 0) p.lse[bh] = M != -INFINITY ? (M + log2f(L)) * LN2 : -INFINITY;
       } else {
         p.part_o[(slot * PD_HEADS + g) * D + d] = acc;
@@ -327,14 +383,14 @@ cudaError_t combine(const PagedDecodeArgs &a, int ctas, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t launch_fp32(const PagedDecodeArgs &a, const InvFreq &inv, cudaStream_t st) {
-  constexpr int ctas = 296;
+cudaError_t launch_fp32(const PagedDecodeArgs &a, const TurnFreq &turn, cudaStream_t st) {
   const int gp = a.GS > PD_HEADS ? PD_HEADS : a.GS;
-  const auto kernel = gp == 1   ? paged_decode_kernel<float, D, 1>
-                      : gp == 2 ? paged_decode_kernel<float, D, 2>
-                      : gp <= 4 ? paged_decode_kernel<float, D, 4>
-                                : paged_decode_kernel<float, D, 8>;
-  const cudaError_t e = launch_overlapped(kernel, ctas, NT, 0, st, a, inv);
+  const int ctas = 148 * ctas_per_sm(gp);
+  const auto kernel = gp == 1   ? paged_decode_kernel<D, 1>
+                      : gp == 2 ? paged_decode_kernel<D, 2>
+                      : gp <= 4 ? paged_decode_kernel<D, 4>
+                                : paged_decode_kernel<D, 8>;
+  const cudaError_t e = launch_overlapped(kernel, ctas, NT, 0, st, a, turn);
   return e != cudaSuccess ? e : combine<float, D>(a, ctas, st);
 }
 
@@ -346,10 +402,9 @@ cudaError_t launch_bf16(const PagedDecodeArgs &a, const TurnFreq &turn, cudaStre
 
 }  // namespace pgd
 
-cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const InvFreq &inv, const TurnFreq &turn,
-                                cudaStream_t st) {
-  if (D == 128) return bf16 ? pgd::launch_bf16<128>(a, turn, st) : pgd::launch_fp32<128>(a, inv, st);
-  return bf16 ? pgd::launch_bf16<64>(a, turn, st) : pgd::launch_fp32<64>(a, inv, st);
+cudaError_t launch_paged_decode(bool bf16, int D, const PagedDecodeArgs &a, const TurnFreq &turn, cudaStream_t st) {
+  if (D == 128) return bf16 ? pgd::launch_bf16<128>(a, turn, st) : pgd::launch_fp32<128>(a, turn, st);
+  return bf16 ? pgd::launch_bf16<64>(a, turn, st) : pgd::launch_fp32<64>(a, turn, st);
 }
 
 }  // namespace jl
