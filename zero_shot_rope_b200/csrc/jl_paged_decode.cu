@@ -34,22 +34,27 @@ __device__ __forceinline__ void load_pairs(const float *row, int half, int lane,
 
 // One warp takes 8 keys (half a 16-key block) of every tile and keeps its own
 // running maximum, sum and output; the warps are merged when the CTA leaves a
-// (sequence, kv head, head block).  The cache is read once, straight into
-// registers: a lane has four channels (two at head_dim 64) of all eight keys.
+// (sequence, kv head, head block).  Each warp has its own ring of STAGES x 8 keys
+// and values in shared memory, filled by asynchronous copies two tiles ahead (and
+// the page looked up before that), so warps never wait for one another on the
+// way.  A lane has four channels (two at head_dim 64) of all eight keys.
 // The 8 keys x 4 heads partial scores are added up over the lanes together (with
 // each shuffle a lane hands over half of what it holds), which leaves one whole
 // score in each lane: every exponential is taken once.  The weights go through
 // shared memory to all lanes.  Four heads at a time bound the registers.
-constexpr int ctas_per_sm(int gp) { return gp <= 4 ? 2 : 1; }  // by their registers
+constexpr int STAGES = 3;
+constexpr int ring_bytes(int D) { return STAGES * NW * 8 * 2 * D * 4; }
+constexpr int ctas_per_sm(int D) { return D == 64 ? 2 : 1; }  // by their rings: 96 and 192 KB
 
 template <int D, int GP>
-__global__ void __launch_bounds__(NT, ctas_per_sm(GP))
+__global__ void __launch_bounds__(NT, ctas_per_sm(D))
 paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_constant__ TurnFreq turn) {
   constexpr int PPL = D / 64, HALF = D / 2, KW = 8;
   constexpr int GC = GP < 4 ? GP : 4, NC = GP / GC;  // heads at a time, and how often
   constexpr int NV = KW * GC;                        // their scores: NV lanes (and copies)
   __shared__ float red_ml[NW][GP][2];
-  __shared__ float red_o[NW][GP][D];
+  extern __shared__ __align__(16) float ring[];  // [STAGES][NW][K, V][KW][D], at the end of a piece the warps' outputs
+  float(*red_o)[GP][D] = reinterpret_cast<float(*)[GP][D]>(ring);
   __shared__ __align__(16) float w_s[NW][KW][GC], f_s[NW][GC];
   let_next_kernel_come();
   wait_for_kernel_before();
@@ -93,28 +98,60 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
 #pragma unroll
     for (int x = 0; x < NC; ++x) m[x] = -INFINITY, l[x] = 0.f;
 
-    int page = 0, jb = paged_block(p, s, b, kvh, u0, warp >> 1, page);
-    for (int u = u0; u < u1; ++u) {
-      const int j0 = jb + (warp & 1) * KW;
-      const bool some = jb >= 0 && j0 < s.L && j0 + KW > s.jw;
-      float ka[KW][PPL], kb[KW][PPL], va[KW][PPL], vb[KW][PPL];
-      if (some) {
-        const size_t row0 = (size_t)page * p.page_stride +
-                            ((size_t)(j0 & ((1 << p.page_log2) - 1)) * p.Hkv + kvh) * D;
+    // the warp's first key in tile u and its place in the pools
+    auto look = [&](int u, int &j0, size_t &row) {
+      int page;
+      j0 = u < u1 ? paged_block(p, s, b, kvh, u, warp >> 1, page) : -1;
+      if (j0 < 0) return;
+      j0 += (warp & 1) * KW;
+      if (j0 >= s.L || j0 + KW <= s.jw) {
+        j0 = -1;
+        return;
+      }
+      row = (size_t)page * p.page_stride + ((size_t)(j0 & ((1 << p.page_log2) - 1)) * p.Hkv + kvh) * D;
+    };
+    auto fetch = [&](int st, int j0, size_t row) {
+      if (j0 >= 0) {
+        constexpr int PIECES = D / 4;  // 16-byte pieces of a row
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + ((st * NW + warp) * 2) * KW * D);
 #pragma unroll
-        for (int x = 0; x < KW; ++x) {
-          if (j0 + x < s.L && j0 + x >= s.jw) {  // other rows may hold anything
-            load_pairs<PPL>((const float *)p.k + row0 + (size_t)x * p.Hkv * D, HALF, lane, ka[x], kb[x]);
-            load_pairs<PPL>((const float *)p.v + row0 + (size_t)x * p.Hkv * D, HALF, lane, va[x], vb[x]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < PPL; ++e) ka[x][e] = kb[x][e] = va[x][e] = vb[x][e] = 0.f;
-          }
+        for (int i = 0; i < KW * PIECES / 32; ++i) {
+          const int x = (i * 32 + lane) / PIECES, c = (i * 32 + lane) % PIECES;
+          const int n = j0 + x < s.L && j0 + x >= s.jw ? 16 : 0;  // other rows may hold anything: zeros
+          const size_t at = n ? row + (size_t)x * p.Hkv * D + c * 4 : 0;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (x * D + c * 4) * 4),
+                       "l"((const float *)p.k + at), "r"(n)
+                       : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + ((KW + x) * D + c * 4) * 4),
+                       "l"((const float *)p.v + at), "r"(n)
+                       : "memory");
         }
       }
-      // the next tile's page, while this tile's rows come
-      if (u + 1 < u1) jb = paged_block(p, s, b, kvh, u + 1, warp >> 1, page);
-      if (!some) continue;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int ja, jb, jc;
+    size_t row;
+    look(u0, ja, row);
+    fetch(0, ja, row);
+    look(u0 + 1, jb, row);
+    fetch(1, jb, row);
+    int st = 0;
+    for (int u = u0; u < u1; ++u) {
+      look(u + 2, jc, row);
+      const int j0 = ja;
+      ja = jb, jb = jc;
+      const int st0 = st, st2 = st == 0 ? 2 : st - 1;  // this tile's stage, and that of two tiles on
+      st = st == 2 ? 0 : st + 1;
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      if (j0 < 0) {
+        fetch(st2, jc, row);
+        continue;
+      }
+      const float *kt = ring + (st0 * NW + warp) * 2 * KW * D, *vt = kt + KW * D;
+      float ka[KW][PPL], kb[KW][PPL];
+#pragma unroll
+      for (int x = 0; x < KW; ++x) load_pairs<PPL>(kt + x * D, HALF, lane, ka[x], kb[x]);
       if (G > 1 && j0 < j_local) {
         // the angle of the first key, the next ones a step of one position or
         // none (j + 1 a multiple of G) further
@@ -193,7 +230,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
         }
 #pragma unroll
         for (int x = 0; x < KW; ++x) {
-          float pg[GC];
+          float pg[GC], va[PPL], vb[PPL];
+          load_pairs<PPL>(vt + x * D, HALF, lane, va, vb);
           if constexpr (GC == 4) {
             const float4 v = *reinterpret_cast<const float4 *>(w_s[warp][x]);
             pg[0] = v.x, pg[1] = v.y, pg[2] = v.z, pg[3] = v.w;
@@ -205,14 +243,17 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
           for (int g = 0; g < GC; ++g)
 #pragma unroll
             for (int e = 0; e < PPL; ++e) {
-              oa[y * GC + g][e] = fmaf(pg[g], va[x][e], oa[y * GC + g][e]);
-              ob[y * GC + g][e] = fmaf(pg[g], vb[x][e], ob[y * GC + g][e]);
+              oa[y * GC + g][e] = fmaf(pg[g], va[e], oa[y * GC + g][e]);
+              ob[y * GC + g][e] = fmaf(pg[g], vb[e], ob[y * GC + g][e]);
             }
         }
       }
+      // (what this stage held is free: the next fetch goes to another one)
+      fetch(st2, jc, row);
     }
 
     // merge the warps
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 #pragma unroll
     for (int y = 0; y < NC; ++y) {
@@ -252,6 +293,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs p, const __grid_cons
         }
       }
     }
+    __syncthreads();  // the rings are free again
   }
 }
 
@@ -385,12 +427,13 @@ cudaError_t combine(const PagedDecodeArgs &a, int ctas, cudaStream_t st) {
 template <int D>
 cudaError_t launch_fp32(const PagedDecodeArgs &a, const TurnFreq &turn, cudaStream_t st) {
   const int gp = a.GS > PD_HEADS ? PD_HEADS : a.GS;
-  const int ctas = 148 * ctas_per_sm(gp);
+  const int ctas = 148 * ctas_per_sm(D);
   const auto kernel = gp == 1   ? paged_decode_kernel<D, 1>
                       : gp == 2 ? paged_decode_kernel<D, 2>
                       : gp <= 4 ? paged_decode_kernel<D, 4>
                                 : paged_decode_kernel<D, 8>;
-  const cudaError_t e = launch_overlapped(kernel, ctas, NT, 0, st, a, turn);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(D));
+  if (e == cudaSuccess) e = launch_overlapped(kernel, ctas, NT, ring_bytes(D), st, a, turn);
   return e != cudaSuccess ? e : combine<float, D>(a, ctas, st);
 }
 
