@@ -16,18 +16,16 @@
 //              values, with the warp's own running maximum and sum; merged when
 //              the run leaves a (sequence, kv head).
 //
-// Products are m16n8k16 in registers, with the query heads as the 16 rows.
-// They need neither tensor memory nor a trip of the turned keys through shared
-// memory: a key's channel k and its partner k + D/2 sit in the same lane (the
-// operand of step kk and that of step kk + D/32), so the rotation happens on the
-// operand's own registers.  At the memory's pace a 128-key tile pair leaves an
-// SM some 2800 cycles; its 384 products take about 770 of them.
+// Products are m16n8k16 in registers: keys x channels by channels x heads for
+// the scores, channels x keys by keys x heads for the outputs.  They need neither
+// tensor memory nor a trip of the turned keys through shared memory: a key's
+// channel k and its partner k + D/2 sit in the same lane (the operand of step x
+// and that of step x + D/32), so the rotation happens on the operand's own
+// registers.  At the memory's pace a tile leaves an SM some 1400 cycles.
 //
-// Precision: the turned key is split into two bf16, hi + lo, and both are
-// multiplied; the eight rows that a group of up to eight heads leaves free carry
-// the low half of the softmax weights in the second product.  So neither the
-// keys nor the weights are rounded to eight bits; scores, maxima, sums and
-// outputs are fp32.
+// Precision: turned keys and softmax weights are split into two bf16, hi + lo,
+// and both are multiplied, so neither is rounded to eight bits; scores, maxima,
+// sums and outputs are fp32.
 #include "jl_paged.cuh"
 #include "jl_ptx.cuh"
 
@@ -92,6 +90,12 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// an 8 x 8 matrix of 16-bit elements, transposed over the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 // Packed fp32 pairs, kept as 64-bit registers from the load to the last use:
 // one instruction computes both lanes.
@@ -281,13 +285,15 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       const int blk = warp & 3, par = warp >> 2;
       const int q4 = lane & 3, row = lane >> 2;
       const float scale = rsqrtf((float)D) * 1.4426950408889634f;
-      // ldmatrix addresses within a tile half: K [key][16-byte chunk], and V the same, transposed on the way
+      // ldmatrix addresses in a tile, of keys x channels and (V, transposed on the
+      // way) channels x keys operands; a box of `rows` keys has 64 channels of each
+      // key in turn, then the other 64
       const int lm = lane >> 3, lr = lane & 7;
-      // (a box of `rows` keys: 64 channels of each key in turn, then the other 64)
       const int rows = min(1 << p.page_log2, PD_TILE);
       const uint32_t half_b = D == 128 ? rows * 128 : 0;
-      const uint32_t kv_row = (uint32_t)(blk * PD_BLK / rows * rows * D * 2 +
-                                         (blk * PD_BLK % rows + (lm >> 1) * 8 + lr) * 128);
+      const uint32_t blk_at = (uint32_t)(blk * PD_BLK / rows * rows * D * 2 + (blk * PD_BLK % rows + lr) * 128);
+      const uint32_t k_at = blk_at + (lm & 1) * 1024, v_at = blk_at + (lm >> 1) * 1024;
+      const int k_ch = lm >> 1, v_ch = lm & 1;  // 8-channel chunk of a 16-channel step
       int it = 0;
       bool ok = true;
       while (w.next(p)) {
@@ -301,7 +307,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
         // by 2^16 / G rounded up where G < 32 (exact for numerators below 2^11), else at most one
         const uint32_t inv_g = G < 32 ? (65535u + G) / G : 0u;
         auto turn_in = [&](int rho, int x) { return x - (G < 32 ? (int)(((rho + x) * inv_g) >> 16) : rho + x >= G); };
-        // query operand: row = head, channels 16 x + 2 q4 + {0, 1} and + 8
+        // query operand: column = head `row`, channels 16 x + 2 q4 + {0, 1} and + 8
         uint32_t qf[D / 16][2];
         {
           const uint32_t *q = reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)p.q +
@@ -312,8 +318,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
             qf[x][1] = row < gh ? q[8 * x + 4 + q4] : 0u;
           }
         }
-        // outputs, transposed: channels 16 x + row and + 8 of heads 2 q4 + {0, 1}; maximum and sum of head `row`
-        float o[D / 16][4], m = -INFINITY, l = 0.f;
+        // outputs, transposed: channels 16 x + row and + 8 of heads 2 q4 + {0, 1}; maximum of and this lane's
+        // part of the sum for those heads
+        float o[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
 
@@ -325,20 +332,20 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           if (!ok) continue;  // the run is walked to its end, so that the merges' barriers are met
           const int j0 = s_j0[st][blk];
           if (j0 >= 0) {
-            const uint32_t kt = sbase + GG::OFF_K + st * GG::KV + kv_row;
-            const uint32_t vt = sbase + GG::OFF_V + st * GG::KV + kv_row;
-            // scores of keys 8 nb + 2 q4 + {0, 1} for head `row` in c[nb][0..1]
-            float sc[2][2];
+            const uint32_t kt = sbase + GG::OFF_K + st * GG::KV + k_at;
+            const uint32_t vt = sbase + GG::OFF_V + st * GG::KV + v_at;
+            // scores of keys `row` (0, 1) and row + 8 (2, 3) for heads 2 q4 and 2 q4 + 1
+            float sc[4];
             auto plain_scores = [&]() {
-              float c[2][4] = {};
+              float c[4] = {}, d[4] = {};
 #pragma unroll
               for (int x = 0; x < D / 16; ++x) {
                 uint32_t kf[4];
-                ldsm4(kt + (x >> 2) * half_b + ((((x & 3) * 2 + (lm & 1)) ^ lr) << 4), kf);
-                mma(c[0], qf[x][0], 0u, qf[x][1], 0u, kf[0], kf[1]);
-                mma(c[1], qf[x][0], 0u, qf[x][1], 0u, kf[2], kf[3]);
+                ldsm4(kt + (x >> 2) * half_b + ((((x & 3) * 2 + k_ch) ^ lr) << 4), kf);
+                mma(x & 1 ? d : c, kf[0], kf[1], kf[2], kf[3], qf[x][0], qf[x][1]);
               }
-              sc[0][0] = c[0][0], sc[0][1] = c[0][1], sc[1][0] = c[1][0], sc[1][1] = c[1][1];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[e] = c[e] + d[e];
             };
             if (j0 >= j_local) {
               plain_scores();
@@ -350,16 +357,16 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
               const uint32_t tab = sbase + GG::OFF_TAB;
               const uint32_t t0 = tab + r0 * HALF * 8, t1 = tab + r1 * HALF * 8;
               const uint32_t x0 = (r0 & 1) * 64, x1 = (r1 & 1) * 64;
-              float c[2][4] = {}, cl[2][4] = {};
+              float c[4] = {}, cl[4] = {};
 #pragma unroll
               for (int x = 0; x < D / 32; ++x) {
                 // channels 16 x .. + 15 and their partners
                 uint32_t ka[4], kb[4];
-                ldsm4(kt + (((x * 2 + (lm & 1)) ^ lr) << 4), ka);
+                ldsm4(kt + (((x * 2 + k_ch) ^ lr) << 4), ka);
                 if constexpr (D == 128)
-                  ldsm4(kt + half_b + (((x * 2 + (lm & 1)) ^ lr) << 4), kb);
+                  ldsm4(kt + half_b + (((x * 2 + k_ch) ^ lr) << 4), kb);
                 else
-                  ldsm4(kt + (((4 + x * 2 + (lm & 1)) ^ lr) << 4), kb);
+                  ldsm4(kt + (((4 + x * 2 + k_ch) ^ lr) << 4), kb);
                 uint32_t ah[4], al[4], bh[4], bl[4];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {  // channels + 8 y
@@ -367,81 +374,86 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
                   uint64_t fc, fs;
                   lds_u64x2(ang + at, fc, fs);
 #pragma unroll
-                  for (int nb = 0; nb < 2; ++nb) {
+                  for (int nb = 0; nb < 2; ++nb) {  // keys + 8 nb
+                    const int i = 2 * y + nb;
                     uint64_t gc, gs;
                     lds_u64x2((nb ? t1 : t0) + ((at + q4 * 16) ^ (nb ? x1 : x0)), gc, gs);
                     const uint64_t co = sub2(mul2(fc, gc), mul2(fs, gs));
                     const uint64_t si = fma2(fs, gc, mul2(fc, gs));
-                    const uint64_t a = bf2_f2(ka[2 * nb + y]), b = bf2_f2(kb[2 * nb + y]);
-                    split2(fma2(a, co, mul2(b, si)), ah[2 * nb + y], al[2 * nb + y]);
-                    split2(sub2(mul2(b, co), mul2(a, si)), bh[2 * nb + y], bl[2 * nb + y]);
+                    const uint64_t a = bf2_f2(ka[i]), b = bf2_f2(kb[i]);
+                    split2(fma2(a, co, mul2(b, si)), ah[i], al[i]);
+                    split2(sub2(mul2(b, co), mul2(a, si)), bh[i], bl[i]);
                   }
                 }
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
-                  mma(c[nb], qf[x][0], 0u, qf[x][1], 0u, ah[2 * nb], ah[2 * nb + 1]);
-                  mma(cl[nb], qf[x][0], 0u, qf[x][1], 0u, al[2 * nb], al[2 * nb + 1]);
-                  mma(c[nb], qf[D / 32 + x][0], 0u, qf[D / 32 + x][1], 0u, bh[2 * nb], bh[2 * nb + 1]);
-                  mma(cl[nb], qf[D / 32 + x][0], 0u, qf[D / 32 + x][1], 0u, bl[2 * nb], bl[2 * nb + 1]);
-                }
+                mma(c, ah[0], ah[1], ah[2], ah[3], qf[x][0], qf[x][1]);
+                mma(cl, al[0], al[1], al[2], al[3], qf[x][0], qf[x][1]);
+                mma(c, bh[0], bh[1], bh[2], bh[3], qf[D / 32 + x][0], qf[D / 32 + x][1]);
+                mma(cl, bl[0], bl[1], bl[2], bl[3], qf[D / 32 + x][0], qf[D / 32 + x][1]);
               }
-              float rot[2][2];
-#pragma unroll
-              for (int nb = 0; nb < 2; ++nb) rot[nb][0] = c[nb][0] + cl[nb][0], rot[nb][1] = c[nb][1] + cl[nb][1];
               if (j0 + PD_BLK > j_local) {  // the one block with keys of both kinds
                 plain_scores();
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    if (j0 + 8 * nb + 2 * q4 + e < j_local) sc[nb][e] = rot[nb][e];
+                for (int e = 0; e < 4; ++e)
+                  if (j0 + row + 8 * (e >> 1) < j_local) sc[e] = c[e] + cl[e];
               } else {
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb) sc[nb][0] = rot[nb][0], sc[nb][1] = rot[nb][1];
+                for (int e = 0; e < 4; ++e) sc[e] = c[e] + cl[e];
               }
             }
             // mask, in units of log2 e
             const bool part = j0 + PD_BLK > L || j0 < jw;
-            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                sc[nb][e] *= scale;
-                if (part) {
-                  const int j = j0 + 8 * nb + 2 * q4 + e;
-                  if (j >= L || j < jw) {
-                    sc[nb][e] = -INFINITY;
-                    keep[nb] &= e == 0 ? 0xffff0000u : 0x0000ffffu;
-                  }
-                }
-              }
-            float top = max_nan(max_nan(sc[0][0], sc[0][1]), max_nan(sc[1][0], sc[1][1]));
-            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the maximum is only moved when it has grown by more than 2^8
-            const bool grow = !(top <= m + 8.f) && !(top == -INFINITY);
-            if (__any_sync(0xffffffffu, grow)) {
-              const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
-              if (grow) m = top;
-              l *= f;
-              const float f0 = __shfl_sync(0xffffffffu, f, 8 * q4), f1 = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
-#pragma unroll
-              for (int x = 0; x < D / 16; ++x) o[x][0] *= f0, o[x][1] *= f1, o[x][2] *= f0, o[x][3] *= f1;
+            for (int e = 0; e < 4; ++e) {
+              sc[e] *= scale;
+              const int j = j0 + row + 8 * (e >> 1);
+              if (part && (j >= L || j < jw)) sc[e] = -INFINITY;
             }
-            const float mu = m == -INFINITY ? 0.f : m;
+            float top[2], f[2];
+            bool grow = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              top[h] = max_nan(sc[h], sc[2 + h]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top[h] = max_nan(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
+              // the maximum is only moved when it has grown by more than 2^8
+              const bool g = !(top[h] <= m[h] + 8.f) && !(top[h] == -INFINITY);
+              f[h] = 1.f;
+              if (g) {
+                f[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - top[h]);
+                m[h] = top[h];
+              }
+              grow = grow || g;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+              l[0] *= f[0], l[1] *= f[1];
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x) o[x][0] *= f[0], o[x][1] *= f[1], o[x][2] *= f[0], o[x][3] *= f[1];
+            }
+            // weights, high and low halves, turned into the second operand of the products with the values
+            const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
             uint32_t ph[2], pl[2];
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb) {
-              const float e0 = ex2(sc[nb][0] - mu), e1 = ex2(sc[nb][1] - mu);
-              l += e0 + e1;
+              const float e0 = ex2(sc[2 * nb] - m0), e1 = ex2(sc[2 * nb + 1] - m1);
+              l[0] += e0, l[1] += e1;
               split2(pack2(e0, e1), ph[nb], pl[nb]);
+              ph[nb] = transpose8(ph[nb]);
+              pl[nb] = transpose8(pl[nb]);
             }
-            // (values^T) (weights^T): a score's lane already holds the weight where the operand wants it
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of keys 2 q4 + {0, 1} (+ 8)
+            if (part) {
+#pragma unroll
+              for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int j = j0 + 8 * nb + 2 * q4 + e;
+                  if (j >= L || j < jw) keep[nb] &= e == 0 ? 0xffff0000u : 0x0000ffffu;
+                }
+            }
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
               uint32_t vf[4];
-              ldsm4t(vt + (x >> 2) * half_b + ((((x & 3) * 2 + (lm & 1)) ^ lr) << 4), vf);
+              ldsm4t(vt + (x >> 2) * half_b + ((((x & 3) * 2 + v_ch) ^ lr) << 4), vf);
               if (part) {  // rows past the length may hold anything, and 0 NaN is NaN
                 vf[0] &= keep[0], vf[1] &= keep[0];
                 vf[2] &= keep[1], vf[3] &= keep[1];
@@ -455,9 +467,12 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
         }
 
         // merge the warps' results of this piece
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (q4 == 0) red_ml[warp][row][0] = m, red_ml[warp][row][1] = l;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+          if (row == 0) red_ml[warp][2 * q4 + h][0] = m[h], red_ml[warp][2 * q4 + h][1] = l[h];
+        }
         float *red = reinterpret_cast<float *>(gbase + GG::OFF_RED);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
