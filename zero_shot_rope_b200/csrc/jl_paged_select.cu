@@ -19,7 +19,6 @@ namespace jl {
 
 namespace pgs {
 
-constexpr int NT_SCORE = 256;
 
 // PPL pairs per lane, as fp32: elements PPL l .. of a row's halves
 template <typename T, int PPL>
@@ -104,7 +103,7 @@ __device__ __forceinline__ void load_n(const T *p, float (&x)[N]) {
   }
 }
 
-// Twice the scores, in fp32.  A CTA takes the key ranges of up to 16 pages and 8
+// Twice the scores, in fp32.  A CTA takes the key ranges of 8 pages and up to 8
 // kv heads, 64 KB at most, all asked for at once (a page's heads lie side by
 // side); the pages' angles are formed meanwhile, once for all heads.  Then warps
 // go through the heads with the head's queries in registers, two pages at a
@@ -112,15 +111,14 @@ __device__ __forceinline__ void load_n(const T *p, float (&x)[N]) {
 // over the lanes together: with each shuffle it hands over half of what it holds
 // and keeps the other half.
 constexpr int SCORE_HEADS = 8;
+constexpr int SP = 8;
 template <typename T, int D>
-__host__ __device__ constexpr int score_pages() { return 2 * D * sizeof(T) <= 512 ? 16 : 8; }
-template <typename T, int D>
-__host__ __device__ constexpr size_t score_smem() { return score_pages<T, D>() * SCORE_HEADS * 2 * D * sizeof(T); }
+__host__ __device__ constexpr int score_smem() { return SP * SCORE_HEADS * 2 * D * (int)sizeof(T); }
 
-template <typename T, int D, int GP>
-__global__ void __launch_bounds__(NT_SCORE, 2)
+template <typename T, int D, int GP, int NT_SCORE>
+__global__ void __launch_bounds__(NT_SCORE, 512 / NT_SCORE)
 score_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__ TurnFreq turn) {
-  constexpr int HALF = D / 2, PPL = HALF / 16, NW = NT_SCORE / 32, SP = score_pages<T, D>();
+  constexpr int HALF = D / 2, PPL = HALF / 16, NW = NT_SCORE / 32;
   extern __shared__ __align__(16) uint8_t range_s[];  // [SP][heads][2][D]
   __shared__ float4 ang[SP][HALF / 2];                // of two neighbouring pairs: cos, cos, sin, sin
   __shared__ const uint8_t *from_s[SP];  // a page's ranges, NULL: not there
@@ -646,15 +644,18 @@ cudaError_t launch(const PagedSelectArgs &args, const InvFreq &inv, const TurnFr
   PagedSelectArgs a = args;
   const int gp = a.GS == 1 ? 1 : a.GS == 2 ? 2 : a.GS <= 4 ? 4 : 8;
   if (a.max_pages > a.n_select) {  // some sequence may have more pages than the list
-    const auto kernel = gp == 1   ? score_kernel<T, D, 1>
-                        : gp == 2 ? score_kernel<T, D, 2>
-                        : gp == 4 ? score_kernel<T, D, 4>
-                                  : score_kernel<T, D, 8>;
-    constexpr int SP = score_pages<T, D>();
+    // Many CTAs: 128 threads each, so that four of them share an SM and one
+    // loads while another computes (32 sequences up to 32K: 34 us against 41).
+    // Fewer than four per SM: 256 threads, for the time of one (128K: 14 us
+    // against 18).
     const dim3 grid((a.max_pages + SP - 1) / SP, a.B, (a.Hkv + SCORE_HEADS - 1) / SCORE_HEADS);
-    cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)score_smem<T, D>());
-    if (e == cudaSuccess) e = launch_overlapped(kernel, grid, NT_SCORE, score_smem<T, D>(), st, a, turn);
+    const bool many = (long long)grid.x * grid.y * grid.z >= 4 * 148;
+#define JL_SCORE(GP) (many ? score_kernel<T, D, GP, 128> : score_kernel<T, D, GP, 256>)
+    const auto kernel = gp == 1 ? JL_SCORE(1) : gp == 2 ? JL_SCORE(2) : gp == 4 ? JL_SCORE(4) : JL_SCORE(8);
+#undef JL_SCORE
+    constexpr int smem = score_smem<T, D>();
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch_overlapped(kernel, grid, many ? 128 : 256, smem, st, a, turn);
     if (e != cudaSuccess) return e;
   }
   // few pages: few threads, whose barriers are short

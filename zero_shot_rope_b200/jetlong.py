@@ -270,17 +270,12 @@ def jl_bifocal_decode_noalloc_error(stream=None) -> int:
 # ABI sees pointers only), run on the device of their tensors whichever is
 # current, and allocate what the caller did not pass on the stream they run on.
 # A generation step makes three of them per layer, so what they do on the host
-# is kept short: each tensor is checked by one expression, and only a misfit is
-# looked at in detail.
+# is kept short: one expression checks the usual case, everything contiguous, and
+# only where it does not hold is each tensor looked at by itself.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_raw_device = getattr(torch._C, "_cuda_getDevice", None)
-
-
-def _device():
-    if _raw_device is not None and torch.cuda.is_initialized():
-        return _raw_device()
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_I32 = torch.int32
 
 # the argument words of jl_paged_call; the packed form costs a fifth of a
 # foreign call with as many arguments
@@ -377,9 +372,8 @@ def _scratch(workspace, nbytes, like):
 def _elsewhere(t, stream):
     """The context that makes t's device, and ``stream`` if there is one,
     current; None where they are already (or t is no CUDA tensor)."""
-    if stream is None and t.get_device() == _device():
-        return None
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0 or (stream is None and index == _raw_device()):
         return None
     if stream is None:
         return torch.cuda.device(t.device)
@@ -388,15 +382,15 @@ def _elsewhere(t, stream):
     return torch.cuda.stream(stream)
 
 
-def _no_host_tensor(t):
-    if not t.is_cuda:
+def _no_host_tensor(t, index):
+    if index < 0:
         raise ValueError(f"tensors must be on a CUDA device (got {t.device})")
 
 
-def _stream_of(t):
+def _stream_of(index):
     if _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, max_new, page_summary=None, q=None,
@@ -414,30 +408,39 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
             return jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, max_new, page_summary, q,
                                    q_out, rope_theta)
     T, Hkv, D = shape = _heads3("k", k)
-    dtype = k.dtype
+    dtype, index = k.dtype, k.get_device()
     code = _dtype_code(k)
     B = seqlens.numel()
-    _tensor("k", k, shape, dtype, k)
-    _tensor("v", v, shape, dtype, k)
-    page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, k)
-    cols, table_stride = _table(block_table, B, k)
-    _tensor("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, k)
-    _tensor("seqlens", seqlens, (B,), torch.int32, k)
+    pool, table = k_pages.shape, block_table.shape
     summary = q_in = q_to = 0
-    if page_summary is not None:
-        _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, k)
-        summary = page_summary.data_ptr()
     Hq = Hkv
     if q is not None:
         if rope_theta is None:
             raise ValueError("q is only rotated: it needs rope_theta")
         Hq = _heads3("q", q)[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if (len(pool) == 4 and pool[0] > 0 and pool[2] == Hkv and pool[3] == D and len(table) == 2 and table[0] == B
+            and k.is_contiguous() and _fits(v, shape, dtype, index) and _fits(k_pages, pool, dtype, index)
+            and _fits(v_pages, pool, dtype, index) and _fits(block_table, table, _I32, index)
+            and _fits(cu_seqlens, (B + 1,), _I32, index) and _fits(seqlens, (B,), _I32, index)):
+        n_pages, page, cols = pool[0], pool[1], table[1]
+        page_stride, table_stride = page * Hkv * D, cols
+    else:
+        _tensor("k", k, shape, dtype, k)
+        _tensor("v", v, shape, dtype, k)
+        page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, k)
+        cols, table_stride = _table(block_table, B, k)
+        _tensor("cu_seqlens", cu_seqlens, (B + 1,), _I32, k)
+        _tensor("seqlens", seqlens, (B,), _I32, k)
+    if page_summary is not None:
+        _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, k)
+        summary = page_summary.data_ptr()
+    if q is not None:
         _tensor("q", q, (T, Hq, D), dtype, k)
         if q_out is not None:
             _tensor("q_out", q_out, (T, Hq, D), dtype, k)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _no_host_tensor(k)
+    _no_host_tensor(k, index)
     if q is not None:
         if q_out is None:
             q_out = torch.empty_like(q)
@@ -446,7 +449,7 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
     _paged_call(0, _APPEND.pack(
         k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), summary, block_table.data_ptr(),
         table_stride, cols, cu_seqlens.data_ptr(), seqlens.data_ptr(), B, T, max_new, Hq, Hkv, D, page, n_pages,
-        page_stride, q_in, q_to, theta, code, flags, _stream_of(k)))
+        page_stride, q_in, q_to, theta, code, flags, _stream_of(index)))
     return q_out
 
 
@@ -466,26 +469,33 @@ def jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_
         with elsewhere:
             return jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_select, w_pretrained,
                                            w0, rope_theta, n_first, n_last, out, flags, workspace)
-    B, Hq, D = _heads3("q", q)
-    dtype = q.dtype
+    B, Hq, D = shape = _heads3("q", q)
+    dtype, index = q.dtype, q.get_device()
     code = _dtype_code(q)
     if page_summary.dim() != 4:
         raise ValueError(f"page_summary must be [n_pages, Hkv, 2, D] (got {list(page_summary.shape)})")
-    n_pages, Hkv, n_select = page_summary.shape[0], page_summary.shape[1], int(n_select)
-    _tensor("q", q, (B, Hq, D), dtype, q)
-    _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, q)
-    cols, table_stride = _table(block_table, B, q)
-    _tensor("seqlens", seqlens, (B,), torch.int32, q)
+    n_pages, Hkv = page_summary.shape[:2]
+    n_select = int(n_select)
+    table = block_table.shape
+    if (len(table) == 2 and table[0] == B and q.is_contiguous()
+            and _fits(page_summary, (n_pages, Hkv, 2, D), dtype, index) and _fits(block_table, table, _I32, index)
+            and _fits(seqlens, (B,), _I32, index)):
+        cols = table_stride = table[1]
+    else:
+        _tensor("q", q, shape, dtype, q)
+        _tensor("page_summary", page_summary, (n_pages, Hkv, 2, D), dtype, q)
+        cols, table_stride = _table(block_table, B, q)
+        _tensor("seqlens", seqlens, (B,), _I32, q)
     if out is not None:
         _tensor("out", out, (B, Hkv, n_select), torch.int32, q)
-    _no_host_tensor(q)
+    _no_host_tensor(q, index)
     if out is None:
         out = q.new_empty((B, Hkv, max(n_select, 0)), dtype=torch.int32)
     keep, ws, ws_bytes = _scratch(workspace, jl_bifocal_select_pages_workspace_size(B, Hkv, cols, n_select), q)
     _paged_call(1, _SELECT.pack(
         q.data_ptr(), page_summary.data_ptr(), block_table.data_ptr(), table_stride, cols, seqlens.data_ptr(),
         B, Hq, Hkv, D, page_size, n_pages, n_select, n_first, n_last, w_pretrained, w0, rope_theta, out.data_ptr(), ws,
-        ws_bytes, code, flags, _stream_of(q)))
+        ws_bytes, code, flags, _stream_of(index)))
     return out
 
 
@@ -506,15 +516,22 @@ def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrai
             return jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrained, w0, rope_theta,
                                            page_list, window, out, lse, flags, workspace)
     B, Hq, D = shape = _heads3("q", q)
-    dtype = q.dtype
+    dtype, index = q.dtype, q.get_device()
     code = _dtype_code(q)
-    if k_pages.dim() != 4:
-        raise ValueError(f"k_pages must be [n_pages, page_size, Hkv, D] (got {list(k_pages.shape)})")
-    Hkv = k_pages.shape[2]
-    _tensor("q", q, shape, dtype, q)
-    page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, q)
-    cols, table_stride = _table(block_table, B, q)
-    _tensor("seqlens", seqlens, (B,), torch.int32, q)
+    pool, table = k_pages.shape, block_table.shape
+    if len(pool) != 4:
+        raise ValueError(f"k_pages must be [n_pages, page_size, Hkv, D] (got {list(pool)})")
+    Hkv = pool[2]
+    if (pool[0] > 0 and pool[3] == D and len(table) == 2 and table[0] == B and q.is_contiguous()
+            and _fits(k_pages, pool, dtype, index) and _fits(v_pages, pool, dtype, index)
+            and _fits(block_table, table, _I32, index) and _fits(seqlens, (B,), _I32, index)):
+        n_pages, page, cols = pool[0], pool[1], table[1]
+        page_stride, table_stride = page * Hkv * D, cols
+    else:
+        _tensor("q", q, shape, dtype, q)
+        page, n_pages, page_stride = _pools(k_pages, v_pages, Hkv, D, q)
+        cols, table_stride = _table(block_table, B, q)
+        _tensor("seqlens", seqlens, (B,), _I32, q)
     listed, n_list = 0, 0
     if page_list is not None:
         n_list = page_list.shape[-1] if page_list.dim() == 3 else 0
@@ -527,12 +544,12 @@ def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrai
         lse_to = lse.data_ptr()
     if out is not None:
         _tensor("out", out, shape, dtype, q)
-    _no_host_tensor(q)
+    _no_host_tensor(q, index)
     if out is None:
         out = torch.empty_like(q)
     keep, ws, ws_bytes = _scratch(workspace, jl_bifocal_decode_paged_workspace_size(B, D), q)
     _paged_call(2, _DECODE.pack(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), table_stride, cols,
         seqlens.data_ptr(), listed, n_list, B, Hq, Hkv, D, page, n_pages, page_stride, w_pretrained, w0, window,
-        rope_theta, out.data_ptr(), lse_to, ws, ws_bytes, code, flags, _stream_of(q)))
+        rope_theta, out.data_ptr(), lse_to, ws, ws_bytes, code, flags, _stream_of(index)))
     return out, lse
