@@ -130,7 +130,7 @@ def check(got, want, tol, what=""):
     fine = np.isfinite(want)
     assert np.array_equal(fine, np.isfinite(got)), f"{what}: not finite elsewhere"
     assert np.array_equal(want[~fine], got[~fine]), what
-    err = np.abs(got - np.where(fine, want, got))
+    err = np.abs(np.where(fine, got, 0.0) - np.where(fine, want, 0.0))
     worst = (err / np.maximum(np.broadcast_to(tol, err.shape), 1e-300))[fine]
     assert worst.size == 0 or worst.max() <= 1.0, f"{what}: {worst.max():.2f} of the tolerance, error {err.max():.3e}"
 

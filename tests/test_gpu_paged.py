@@ -572,3 +572,62 @@ def test_decode_at_full_pace_repeats(D, page):
     for _ in range(200):
         again, _ = J.jl_bifocal_decode_paged(q, kp, vp, table, ld, 1 << 20, 64, 1e4)
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("dtype,page", [(BF, 64), (F32, 32)])
+def test_pools_past_32_bit_offsets(dtype, page):
+    # pages whose first element lies past 2^31, with the largest w_pretrained and
+    # w0: everything is local; then turned keys at far positions of a wide table
+    J = jl()
+    Hkv, D = 8, 128
+    n = (1 << 31) // (page * Hkv * D) + 40
+    pool = torch.empty(n, 2, page, Hkv, D, dtype=dtype, device=DEV)
+    kp, vp = pool[:, 0], pool[:, 1]
+    L = 5 * page + 3
+    pages = torch.tensor([n - 1, n - 7, n // 2 + 5, n - 2, 0, n - 30], dtype=torch.int32)
+    g = torch.Generator().manual_seed(1)
+    k, v, q = (torch.randn(L if h == Hkv else 1, h, D, generator=g).to(dtype) for h in (Hkv, Hkv, 16))
+    sm = torch.zeros(n, Hkv, 2, D, dtype=dtype, device=DEV)
+    J.jl_paged_append(k.to(DEV), v.to(DEV), kp, vp, i32(pages[None]), i32([0, L]), i32([L]), L, page_summary=sm)
+    for w_pre, w0 in ((2 ** 63 - 1, 2 ** 31 - 1), (100, 40)):
+        out, lse = run_decode(q, kp, vp, pages[None], (L,), w_pre, w0, 1e4)
+        ro, rl, to, tl = P.decode(q, [k], [v], w_pre, w0, 1e4)
+        P.check(out, ro, to, "out")
+        P.check(lse, rl, tl, "lse")
+        got = J.jl_bifocal_select_pages(q.to(DEV), sm, i32(pages[None]), i32([L]), page, 3, w_pre, w0, 1e4)
+        assert np.array_equal(got.cpu().numpy(), P.select(q, sm.cpu(), pages[None], [L], page, 3, 1, 1, w_pre, w0, 1e4))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_keys_at_far_positions(dtype):
+    # a table of 2^30 / 256 pages, most of them one and the same, listed pages at
+    # its far end: positions near 2^30, G in the thousands
+    J = jl()
+    page, Hkv, D, w_pre, w0 = 256, 1, 128, 40000, 300
+    cols = (1 << 30) // page
+    L = (1 << 30) - 77
+    g = torch.Generator().manual_seed(2)
+    kp, vp = (torch.randn(6, page, Hkv, D, generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(1, 4, D, generator=g).to(dtype)
+    table = torch.zeros(1, cols, dtype=torch.int32)
+    want = [3, 70000, cols // 2 + 1, cols - 3, cols - 2, cols - 1]
+    for x, c in enumerate(want):
+        table[0, c] = x
+    lists = torch.tensor(want, dtype=torch.int32).view(1, 1, -1)
+    out, lse = run_decode(q, kp.to(DEV), vp.to(DEV), table, (L,), w_pre, w0, 1e4, page_list=i32(lists))
+    # the plain form, on the listed keys alone
+    pos = np.concatenate([np.arange(c * page, (c + 1) * page) for c in want])
+    seen = pos < L
+    G = P.group(L, w_pre)
+    shift = np.where(pos < L - w0, (pos // G - pos) - ((L - 1) // G - (L - 1)), 0)[seen]
+    raw, vv = P.f64(kp).reshape(-1, D)[seen], P.f64(vp).reshape(-1, D)[seen]
+    kk = P.rotate(raw, shift, 1e4)
+    for h in range(4):
+        s = kk @ P.f64(q)[0, h] / np.sqrt(D)
+        e = np.exp(s - s.max())
+        size = (P.pair_len(raw) @ np.abs(P.f64(q)[0, h])).max() / np.sqrt(D)
+        # the angle itself, n w, is known to n w 2^-53 and the turn to 2^-32
+        ds, dw = P.slack(size * (1 + (2.0 ** 30 * 2.0 ** -52 + 2 * np.pi * 2.0 ** -32) / (160 * P.U)), abs(s).max(),
+                         len(s), dtype == BF)
+        ref = e @ vv / e.sum()
+        P.check(out[0, h], ref, dw * np.abs(vv).max() + (2.0 ** -8 if dtype == BF else P.U) * np.abs(ref), f"head {h}")

@@ -141,6 +141,9 @@ jl_status check_pool(int32_t page_size, int64_t page_stride, int32_t Hkv, int32_
   return JL_OK;
 }
 
+// No length exceeds 2^30, so every larger w_pretrained means G = 1.
+int64_t longest(int64_t w_pretrained) { return w_pretrained < ((int64_t)1 << 31) ? w_pretrained : (int64_t)1 << 31; }
+
 int log2_of(int32_t x) {
   int l = 0;
   while ((1 << l) < x) ++l;
@@ -432,7 +435,7 @@ jl_status jl_bifocal_select_pages(const void *q, const void *page_summary, const
   a.n_select = n_select;
   a.n_first = n_first;
   a.n_last = n_last;
-  a.w_pre = w_pretrained;
+  a.w_pre = longest(w_pretrained);
   a.w0 = w0;
   a.plain = (flags & JL_FLAG_PLAIN_CAUSAL) ? 1 : 0;
   a.list = page_list;
@@ -501,7 +504,7 @@ jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void
   a.Hkv = n_kv_heads;
   a.GS = n_q_heads / n_kv_heads;
   a.HB = (a.GS + jl::PD_HEADS - 1) / jl::PD_HEADS;
-  a.w_pre = w_pretrained;
+  a.w_pre = longest(w_pretrained);
   a.w0 = w0;
   a.window = window;
   a.plain = (flags & JL_FLAG_PLAIN_CAUSAL) ? 1 : 0;

@@ -146,7 +146,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
   __shared__ int s_j0[NST][NBLK], s_rho[NST][NBLK];  // a block's first key, and its remainder by G
   __shared__ float red_ml[NCW][PD_HEADS][2];
   __shared__ volatile int abort_flag;
-  __shared__ int err_s;
+  __shared__ int err_s, issued;  // tiles whose loads were issued
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (su32(smem_raw) + 1023u) & ~1023u;
   uint8_t *gbase = smem_raw + (sbase - su32(smem_raw));
@@ -157,7 +157,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       mbar_init(&bar_empty[s], NBLK);   // the four consumer warps of the tile
     }
     abort_flag = 0;
-    err_s = 0;
+    err_s = issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // turns by r = 0 .. 15 positions: {cos, cos, sin, sin} of two neighbouring
@@ -224,10 +224,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           }
         }
       }
-      // after a timeout, let the loads in flight land
-      if (!ok)
-        for (int x = max(0, it - NST); x < it; ++x)
-          wait_drain(&bar_full[x % NST], (x / NST) & 1, &err_s, ERR_TIMEOUT);
+      if (lane == 0) issued = it;
     } else if (warp >= WARP_ANGLE) {
       // ======================= angles =======================
       // one warp per consumer group (so that it too sees every phase of its
@@ -516,6 +513,11 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
     }
   }
   __syncthreads();
+  // after a timeout, let the loads in flight land (some role may have left a
+  // stage's barrier incomplete: these waits end too)
+  if (threadIdx.x == 0 && abort_flag)
+    for (int x = max(0, issued - NST); x < issued; ++x)
+      wait_drain(&bar_full[x % NST], (x / NST) & 1, &err_s, ERR_TIMEOUT);
   if (threadIdx.x == 0) p.cta_err[blockIdx.x] = err_s;
 }
 
