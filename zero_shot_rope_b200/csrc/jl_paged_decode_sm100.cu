@@ -181,8 +181,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
     if (warp == WARP_LOAD) {
       // ======================= producer =======================
       const int rows = min(1 << p.page_log2, PD_TILE);  // rows of a box
-      const int runs = PD_TILE / rows;                  // boxes of K (and of V) of a tile
       const int per = rows / PD_BLK;                    // blocks of a box
+      const bool leads = (lane & 3) % per == 0;         // this lane's block is the first of its box
+      const uint32_t to = sbase + (lane & 3) / per * rows * D * 2;
       int it = 0;
       bool ok = true;
       while (ok && w.next(p)) {
@@ -191,36 +192,30 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           // lane: block lane % 4 of tile u + lane / 4
           int page = 0, j0 = -1;
           if (u + (lane >> 2) < w.u1) j0 = paged_block(p, w.s, w.b, kvh, u + (lane >> 2), lane & 3, page);
+          // a box is loaded where any of its blocks is wanted; page and slot are those of the first such block
+          const unsigned want = __ballot_sync(0xffffffffu, j0 >= 0) >> lane & ((1u << per) - 1u);
+          const int src = lane + (want ? __ffs(want) - 1 : 0);
+          const int bp = __shfl_sync(0xffffffffu, page, src), bj = __shfl_sync(0xffffffffu, j0, src);
+          const int slot = (bj & ((1 << p.page_log2) - 1)) & ~(rows - 1);
+          const unsigned boxes = __ballot_sync(0xffffffffu, leads && want != 0);
           for (int x = 0; x < 8 && u + x < w.u1; ++x, ++it) {
             const int st = it % NST;
             if (it >= NST) ok = wait_b(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if ((lane >> 2) == x) s_j0[st][lane & 3] = j0;
-            // a box is loaded where any of its blocks is wanted
-            const unsigned want = (__ballot_sync(0xffffffffu, j0 >= 0) >> (4 * x)) & 15u;
-            int boxes = 0;
-            for (int r = 0; r < runs; ++r) boxes += ((want >> (r * per)) & ((1u << per) - 1u)) != 0;
+            const bool mine = (lane >> 2) == x;
+            if (mine) s_j0[st][lane & 3] = j0;
             __syncwarp();
+            const int n = __popc(boxes >> (4 * x) & 15u);
             if (lane == 0) {
-              if (boxes > 0) mbar_expect_tx(&bar_full[st], (uint32_t)(boxes * rows * D * 2 * 2));
+              if (n > 0) mbar_expect_tx(&bar_full[st], (uint32_t)(n * rows * D * 2 * 2));
               else mbar_arrive(&bar_full[st]);
             }
             __syncwarp();
-            // lane r loads box r: the block it takes page and slot from
-            int src = 0;
-            if (lane < runs) {
-              const unsigned mine = (want >> (lane * per)) & ((1u << per) - 1u);
-              src = 4 * x + lane * per + (mine ? __ffs(mine) - 1 : 0);
+            if (mine && leads && want != 0) {
+              tma_load5(&mK, &bar_full[st], to + GG::OFF_K + st * GG::KV, 0, kvh, slot, bp, 0);
+              tma_load5(&mV, &bar_full[st], to + GG::OFF_V + st * GG::KV, 0, kvh, slot, bp, 0);
             }
-            const int bp = __shfl_sync(0xffffffffu, page, src), bj = __shfl_sync(0xffffffffu, j0, src);
-            if (lane < runs && bj >= 0) {
-              const int slot = (bj & ((1 << p.page_log2) - 1)) & ~(rows - 1);
-              const uint32_t to = sbase + st * GG::KV + lane * rows * D * 2;
-              tma_load5(&mK, &bar_full[st], to + GG::OFF_K, 0, kvh, slot, bp, 0);
-              tma_load5(&mV, &bar_full[st], to + GG::OFF_V, 0, kvh, slot, bp, 0);
-            }
-            __syncwarp();
           }
         }
       }
