@@ -377,7 +377,8 @@ jl_status jl_paged_append(const void *k, const void *v, void *k_pages,
  *              wins a tie.
  *   n_select >= 1;  n_first, n_last >= 0, n_first + n_last <= n_select
  *   workspace  >= jl_bifocal_select_pages_workspace_size(...) bytes, 256-byte
- *              aligned, no initialisation needed
+ *              aligned, no initialisation needed.  Calls that overlap on the
+ *              GPU need one each.
  * L_b = 0, or a length past max_pages P, lists nothing.
  */
 size_t jl_bifocal_select_pages_workspace_size(int32_t batch,

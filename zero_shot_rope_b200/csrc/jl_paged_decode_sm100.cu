@@ -70,6 +70,38 @@ __device__ __forceinline__ void tma_load5(const CUtensorMap *map, uint64_t *bar,
       "l"(map), "r"(su32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
+// Bounded waits whose probe may suspend the warp for up to SUSPEND_NS (a hint)
+// before it gives the answer: warps that poll take issue slots from those that
+// turn keys (16 x 32K tokens: 398 us with the default, 385 us so).
+constexpr uint32_t SUSPEND_NS = 2000;
+__device__ __forceinline__ bool mbar_try_long(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity), "r"(SUSPEND_NS)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool wait_long_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err) {
+  const uint64_t t0 = gtime();
+  const uint64_t limit = *(volatile unsigned long long *)&g_wait_limit_ns;
+  for (;;) {
+    if (mbar_try_long(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (gtime() - t0 > limit) {
+      *abort_flag = 1;
+      atomicOr(err, ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err) {
+  if (mbar_try_long(bar, parity)) return true;
+  return wait_long_slow(bar, parity, abort_flag, err);
+}
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -200,7 +232,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           const unsigned boxes = __ballot_sync(0xffffffffu, leads && want != 0);
           for (int x = 0; x < 8 && u + x < w.u1; ++x, ++it) {
             const int st = it % NST;
-            if (it >= NST) ok = wait_b(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
+            if (it >= NST) ok = wait_long(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const bool mine = (lane >> 2) == x;
@@ -225,6 +257,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       // one warp per consumer group (so that it too sees every phase of its
       // stages); the angles are formed before the stage is free for them
       const int par = warp - WARP_ANGLE;
+      unsigned long long tw[HALF / 32];
+#pragma unroll
+      for (int e = 0; e < HALF / 32; ++e) tw[e] = turn.v[lane + 32 * e];
       int it = 0;
       bool ok = true;
       while (ok && w.next(p)) {
@@ -248,10 +283,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
               for (int blk = 0; blk < NBLK; ++blk) {
                 const int nb = __shfl_sync(0xffffffffu, n, 4 * x + blk);
 #pragma unroll
-                for (int e = 0; e < HALF / 32; ++e) turn_cs(nb, turn.v[lane + 32 * e], c[blk][e], s[blk][e]);
+                for (int e = 0; e < HALF / 32; ++e) turn_cs(nb, tw[e], c[blk][e], s[blk][e]);
               }
             }
-            if (it >= NST) ok = wait_b(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
+            if (it >= NST) ok = wait_long(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (any) {
@@ -319,7 +354,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
         for (int u = w.u0; u < w.u1; ++u, ++it) {
           if ((it & 1) != par) continue;
           const int st = it % NST;
-          if (ok) ok = wait_b(&bar_full[st], (it / NST) & 1, &abort_flag, &err_s, ERR_TIMEOUT);
+          if (ok) ok = wait_long(&bar_full[st], (it / NST) & 1, &abort_flag, &err_s);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;  // the run is walked to its end, so that the merges' barriers are met
           const int j0 = s_j0[st][blk];
