@@ -73,6 +73,10 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
   float4(*cs)[HALF / 2] = reinterpret_cast<float4(*)[HALF / 2]>(smem);
   float(*red)[NT] = reinterpret_cast<float(*)[NT]>(smem);
   const int b = blockIdx.z, h0 = blockIdx.y * HEADS, heads = min(HEADS, a.Hkv - h0);
+  // (a thread's angles are all of one frequency, read once: lanes that read
+  // different constants take turns)
+  static_assert(NT % HALF == 0, "one frequency per thread");
+  const unsigned long long w = ROT ? turn.v[threadIdx.x % HALF] : 0;
   let_next_kernel_come();
   wait_for_kernel_before();
   const int c0 = a.cu[b], n = a.cu[b + 1] - c0, L = a.seqlens[b];
@@ -114,7 +118,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
       for (int idx = threadIdx.x; idx < m * HALF; idx += NT) {
         const int x = idx / HALF, k = idx % HALF;
         float c, s;
-        turn_cs(j0 + x, turn.v[k], c, s);
+        turn_cs(j0 + x, w, c, s);
         float *to = reinterpret_cast<float *>(&cs[x][k / 2]) + (k & 1);
         to[0] = c;
         to[2] = s;

@@ -195,10 +195,12 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
   // turns by r = 0 .. 15 positions: {cos, cos, sin, sin} of two neighbouring
   // pairs, the 64-byte halves of odd rows swapped so that two rows meet in
   // different banks
-  for (int idx = threadIdx.x; idx < PD_BLK * HALF; idx += THREADS) {
+  constexpr int TT = THREADS / HALF * HALF;  // a thread's turns are all of one frequency
+  const unsigned long long tf = turn.v[threadIdx.x % HALF];
+  for (int idx = threadIdx.x < TT ? threadIdx.x : PD_BLK * HALF; idx < PD_BLK * HALF; idx += TT) {
     const int r = idx / HALF, k = idx % HALF;
     float c, s;
-    turn_cs(r, turn.v[k], c, s);
+    turn_cs(r, tf, c, s);
     float *to = reinterpret_cast<float *>(gbase + GG::OFF_TAB + r * HALF * 8 + (((k >> 1) * 16) ^ ((r & 1) * 64)));
     to[k & 1] = c;
     to[2 + (k & 1)] = s;

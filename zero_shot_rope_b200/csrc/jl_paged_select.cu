@@ -125,6 +125,10 @@ score_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__ 
   __shared__ int turn_s[SP], np_s;
   const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * SP;
   const int h_first = blockIdx.z * SCORE_HEADS, heads = min(SCORE_HEADS, p.Hkv - h_first);
+  // (a thread's angles are all of one frequency, read once: lanes that read
+  // different constants take turns)
+  static_assert(NT_SCORE % HALF == 0, "one frequency per thread");
+  const unsigned long long w = turn.v[threadIdx.x % HALF];
   let_next_kernel_come();
   wait_for_kernel_before();
   if (warp == 0) {
@@ -162,7 +166,7 @@ score_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__ 
   for (int x = threadIdx.x; x < SP * HALF; x += NT_SCORE) {
     const int c = x / HALF, k = x % HALF;
     float co, si;
-    turn_cs(turn_s[c], turn.v[k], co, si);
+    turn_cs(turn_s[c], w, co, si);
     float *to = reinterpret_cast<float *>(&ang[c][k / 2]) + (k & 1);
     to[0] = co;
     to[2] = si;
