@@ -8,6 +8,7 @@ fallback: if ``libjetlong.so`` is missing, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -285,7 +286,13 @@ _DECODE = struct.Struct("=19qd7q")
 
 
 def _paged_call(call, words):
-    _check(lib().jl_paged_call(call, words, len(words) // 8))
+    status = (_lib or lib()).jl_paged_call(call, words, len(words) // 8)
+    if status:
+        _check(status)
+
+
+def _plain(t, dtype, index):
+    return t.dtype is dtype and t.get_device() == index and t.is_contiguous()
 
 
 def _fits(t, shape, dtype, index):
@@ -371,10 +378,9 @@ def _scratch(workspace, nbytes, like):
 
 def _elsewhere(t, stream):
     """The context that makes t's device, and ``stream`` if there is one,
-    current; None where they are already (or t is no CUDA tensor)."""
-    index = t.get_device()
-    if index < 0 or (stream is None and index == _raw_device()):
-        return None
+    current."""
+    if not t.is_cuda:
+        return contextlib.nullcontext()
     if stream is None:
         return torch.cuda.device(t.device)
     if stream.device != t.device:
@@ -402,13 +408,14 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
     are rotated by their positions; without it k is stored as given.
     ``page_summary`` [n_pages, Hkv, 2, D], if given, is kept up to date.
     Returns the rotated q (``q_out``; it may be q itself) or None."""
-    elsewhere = _elsewhere(k, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    index = k.get_device()
+    if stream is not None or (index >= 0 and index != _raw_device()):
+        with _elsewhere(k, stream):
             return jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, max_new, page_summary, q,
                                    q_out, rope_theta)
-    T, Hkv, D = shape = _heads3("k", k)
-    dtype, index = k.dtype, k.get_device()
+    shape = k.shape
+    T, Hkv, D = shape if len(shape) == 3 else _heads3("k", k)
+    dtype = k.dtype
     code = _dtype_code(k)
     B = seqlens.numel()
     pool, table = k_pages.shape, block_table.shape
@@ -421,8 +428,8 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
     elif q_out is not None:
         raise ValueError("q_out without q")
     if (len(pool) == 4 and pool[0] > 0 and pool[2] == Hkv and pool[3] == D and len(table) == 2 and table[0] == B
-            and k.is_contiguous() and _fits(v, shape, dtype, index) and _fits(k_pages, pool, dtype, index)
-            and _fits(v_pages, pool, dtype, index) and _fits(block_table, table, _I32, index)
+            and k.is_contiguous() and _fits(v, shape, dtype, index) and _plain(k_pages, dtype, index)
+            and _fits(v_pages, pool, dtype, index) and _plain(block_table, _I32, index)
             and _fits(cu_seqlens, (B + 1,), _I32, index) and _fits(seqlens, (B,), _I32, index)):
         n_pages, page, cols = pool[0], pool[1], table[1]
         page_stride, table_stride = page * Hkv * D, cols
@@ -464,13 +471,14 @@ def jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_
     first, the ``n_last`` newest and the highest scored others of every kv
     head, ascending, -1 behind the last: int32 [B, Hkv, n_select], for
     jl_bifocal_decode_paged.  q [B, Hq, D] at position seqlens[b] - 1."""
-    elsewhere = _elsewhere(q, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    index = q.get_device()
+    if stream is not None or (index >= 0 and index != _raw_device()):
+        with _elsewhere(q, stream):
             return jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_select, w_pretrained,
                                            w0, rope_theta, n_first, n_last, out, flags, workspace)
-    B, Hq, D = shape = _heads3("q", q)
-    dtype, index = q.dtype, q.get_device()
+    shape = q.shape
+    B, Hq, D = shape if len(shape) == 3 else _heads3("q", q)
+    dtype = q.dtype
     code = _dtype_code(q)
     if page_summary.dim() != 4:
         raise ValueError(f"page_summary must be [n_pages, Hkv, 2, D] (got {list(page_summary.shape)})")
@@ -478,7 +486,7 @@ def jl_bifocal_select_pages(q, page_summary, block_table, seqlens, page_size, n_
     n_select = int(n_select)
     table = block_table.shape
     if (len(table) == 2 and table[0] == B and q.is_contiguous()
-            and _fits(page_summary, (n_pages, Hkv, 2, D), dtype, index) and _fits(block_table, table, _I32, index)
+            and _fits(page_summary, (n_pages, Hkv, 2, D), dtype, index) and _plain(block_table, _I32, index)
             and _fits(seqlens, (B,), _I32, index)):
         cols = table_stride = table[1]
     else:
@@ -510,21 +518,22 @@ def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrai
     seqlens[b] - 1 against the pages of block_table [B, max_pages]; only those
     of ``page_list`` [B, Hkv, n] if given, only the last ``window`` keys if
     not 0.  Returns (out [B, Hq, D], lse [B, Hq] or None)."""
-    elsewhere = _elsewhere(q, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    index = q.get_device()
+    if stream is not None or (index >= 0 and index != _raw_device()):
+        with _elsewhere(q, stream):
             return jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seqlens, w_pretrained, w0, rope_theta,
                                            page_list, window, out, lse, flags, workspace)
-    B, Hq, D = shape = _heads3("q", q)
-    dtype, index = q.dtype, q.get_device()
+    shape = q.shape
+    B, Hq, D = shape if len(shape) == 3 else _heads3("q", q)
+    dtype = q.dtype
     code = _dtype_code(q)
     pool, table = k_pages.shape, block_table.shape
     if len(pool) != 4:
         raise ValueError(f"k_pages must be [n_pages, page_size, Hkv, D] (got {list(pool)})")
     Hkv = pool[2]
     if (pool[0] > 0 and pool[3] == D and len(table) == 2 and table[0] == B and q.is_contiguous()
-            and _fits(k_pages, pool, dtype, index) and _fits(v_pages, pool, dtype, index)
-            and _fits(block_table, table, _I32, index) and _fits(seqlens, (B,), _I32, index)):
+            and _plain(k_pages, dtype, index) and _fits(v_pages, pool, dtype, index)
+            and _plain(block_table, _I32, index) and _fits(seqlens, (B,), _I32, index)):
         n_pages, page, cols = pool[0], pool[1], table[1]
         page_stride, table_stride = page * Hkv * D, cols
     else:
