@@ -37,14 +37,20 @@ __device__ __forceinline__ void load_pairs(const T *row, int half, int lane, flo
   }
 }
 
+// pages of sequence b; 0 for a length outside the contract
+__device__ __forceinline__ int pages_of(const PagedSelectArgs &p, int b) {
+  const int L = p.seqlens[b];
+  if (L < 0 || (long long)L > ((long long)p.max_pages << p.page_log2)) return 0;
+  return (int)(((long long)L + (1 << p.page_log2) - 1) >> p.page_log2);
+}
+// and what its pages' turns depend on
 struct Seq {
   int L, pages, G, ni, j_local;
 };
 __device__ __forceinline__ Seq seq_of(const PagedSelectArgs &p, int b) {
   Seq s;
-  s.L = p.seqlens[b];
-  if (s.L < 0 || (long long)s.L > ((long long)p.max_pages << p.page_log2)) s.L = 0;  // outside the contract: no page
-  s.pages = (int)(((long long)s.L + (1 << p.page_log2) - 1) >> p.page_log2);
+  s.pages = pages_of(p, b);
+  s.L = s.pages > 0 ? p.seqlens[b] : 0;
   s.G = p.plain ? 1 : (int)group_size(s.L, p.w_pre);
   s.ni = s.L > 0 ? corr_n(s.L - 1, s.G) : 0;
   s.j_local = (int)max(0LL, (long long)s.L - (long long)p.w0);
@@ -408,16 +414,30 @@ __device__ int block_scan(int x, int *total) {
 }
 
 // Of R keys per thread (whole numbers, 0: none): the k-th largest, by the whole
-// block, two bits at a time from the top.  Once exactly k keys are at or above
-// a threshold, the least of them is it.
+// block, two bits at a time from the first in which they differ.  Once exactly k
+// keys are at or above a threshold, the least of them is it.
 template <int NT_SEL, int R>
 __device__ uint32_t kth_largest_held(const uint32_t (&key)[R], int k) {
   constexpr int NW = NT_SEL / 32;
   __shared__ uint64_t s_count[2][NW];
-  __shared__ uint32_t s_least[NW];
+  __shared__ uint32_t s_least[NW], s_range[2][NW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t prefix = 0;
-  for (int shift = 30, round = 0; shift >= 0; shift -= 2, round ^= 1) {
+  uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+  for (int x = 0; x < R; ++x) {
+    if (key[x] != 0) lo = min(lo, key[x]);
+    hi = max(hi, key[x]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) s_range[0][warp] = lo, s_range[1][warp] = hi;
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, lane < NW ? s_range[0][lane] : 0xffffffffu);
+  hi = __reduce_max_sync(0xffffffffu, lane < NW ? s_range[1][lane] : 0u);
+  if (lo == hi) return lo;
+  const int first = (31 - __clz(lo ^ hi)) & ~1;  // the two bits from here: the first that differ among them
+  uint32_t prefix = first == 30 ? 0u : hi >> (first + 2) << (first + 2);
+  for (int shift = first, round = 0; shift >= 0; shift -= 2, round ^= 1) {
     // how many keys are at or above prefix + 1, 2, 3 << shift
     int n1 = 0, n2 = 0, n3 = 0;
 #pragma unroll
@@ -475,29 +495,29 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_kernel_come();
   wait_for_kernel_before();
-  const Seq s = seq_of(p, b);
+  const int pages = pages_of(p, b);
   const size_t row = (size_t)b * p.Hkv + h;
   int32_t *list = p.list + row * p.n_select;
-  if (s.pages <= p.n_select) {
-    for (int x = tid; x < p.n_select; x += NT_SEL) list[x] = x < s.pages ? x : -1;
+  if (pages <= p.n_select) {
+    for (int x = tid; x < p.n_select; x += NT_SEL) list[x] = x < pages ? x : -1;
     return;
   }
   float *score = p.score + row * p.max_pages;
   // candidates: the pages between the first ones and the newest
-  const int lo = p.n_first, n = s.pages - p.n_first - p.n_last, k = p.n_select - p.n_first - p.n_last;
-  const bool held = s.pages <= R * NT_SEL;
+  const int lo = p.n_first, n = pages - p.n_first - p.n_last, k = p.n_select - p.n_first - p.n_last;
+  const bool held = pages <= R * NT_SEL;
   // thread: pages R tid .. R tid + R - 1
   float mine[R];
   uint32_t key[R];
   if (held) {
 #pragma unroll
-    for (int x = 0; x < R; ++x) mine[x] = R * tid + x < s.pages ? score[R * tid + x] : -INFINITY;
+    for (int x = 0; x < R; ++x) mine[x] = R * tid + x < pages ? score[R * tid + x] : -INFINITY;
   }
   float above_t = INFINITY, below_t = INFINITY;  // chosen above the one, undecided from the other on
   if (k > 0) {
     // eps
     float size = 0.f;
-    for (int x = tid; x < (s.pages + 1) / 2; x += NT_SEL) size = max_nan(size, p.size[row * p.max_pages + x]);
+    for (int x = tid; x < (pages + 1) / 2; x += NT_SEL) size = max_nan(size, p.size[row * p.max_pages + x]);
     float qs = 0.f;
     const T *q = (const T *)p.q + row * p.GS * D;
     for (int g = warp; g < p.GS; g += NW) {
@@ -539,7 +559,7 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
 #pragma unroll
     for (int x = 0; x < R; ++x) {
       const int c = R * tid + x;
-      const bool in = c < s.pages, forced = in && (c < lo || c >= lo + n);
+      const bool in = c < pages, forced = in && (c < lo || c >= lo + n);
       const bool top = in && k > 0 && mine[x] > above_t, near = in && k > 0 && !top && mine[x] >= below_t;
       near_s[x] = near && !forced;
       yes[x] = forced || top || near;
@@ -563,7 +583,7 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
         if (near_s[x]) s_und[x1++] = R * tid + x;
       __syncthreads();
       for (int x = warp; x < und; x += NW) {
-        const double v = score64<T, D>(p, inv, s, b, h, s_und[x], lane);
+        const double v = score64<T, D>(p, inv, seq_of(p, b), b, h, s_und[x], lane);
         if (lane == 0) s_fine[x] = v;
       }
       __syncthreads();
@@ -591,11 +611,11 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
   double *fine = p.fine + row * p.max_pages;
   int32_t *amb = p.amb + row * p.max_pages;
   int sure = 0, und = 0;
-  for (int x0 = 0; x0 < s.pages; x0 += NT_SEL) {
+  for (int x0 = 0; x0 < pages; x0 += NT_SEL) {
     const int c = x0 + tid;
     bool yes = false, maybe = false;
-    if (c < s.pages) {
-      const bool forced = c < lo || c >= s.pages - p.n_last;
+    if (c < pages) {
+      const bool forced = c < lo || c >= pages - p.n_last;
       const float v = score[c];
       yes = forced || (k > 0 && v > above_t);
       maybe = !yes && k > 0 && v >= below_t;
@@ -614,7 +634,7 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
     for (int x = tid; x < und; x += NT_SEL) mark[amb[x]] = 1.f;
   } else if (need > 0) {
     for (int x = warp; x < und; x += NT_SEL / 32) {
-      const double v = score64<T, D>(p, inv, s, b, h, amb[x], lane);
+      const double v = score64<T, D>(p, inv, seq_of(p, b), b, h, amb[x], lane);
       if (lane == 0) fine[x] = v;
     }
     __syncthreads();
@@ -633,9 +653,9 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
   }
   __syncthreads();
   int out = 0;
-  for (int x0 = 0; x0 < s.pages; x0 += NT_SEL) {
+  for (int x0 = 0; x0 < pages; x0 += NT_SEL) {
     const int c = x0 + tid;
-    const bool yes = c < s.pages && mark[c] != 0.f;
+    const bool yes = c < pages && mark[c] != 0.f;
     int sum;
     const int at = block_scan<NT_SEL>(yes ? 1 : 0, &sum);
     if (yes) list[out + at] = c;
