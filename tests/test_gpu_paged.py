@@ -199,6 +199,10 @@ APPEND = [
     ((1000, 513), (700, 500), 256, 4, 4, 128, F32),
     ((33, 100, 17), (33, 1, 2), 16, 6, 2, 64, F32),
     ((131072,), (100,), 64, 32, 8, 128, BF),
+    # enough pages for all heads of one to share a CTA: 256 threads, then 128
+    ((5003,), (5000,), 16, 16, 8, 128, BF),
+    ((5003,), (4999,), 16, 20, 10, 64, F32),
+    ((3001, 2500), (3001, 2400), 16, 2, 2, 64, BF),
 ]
 
 

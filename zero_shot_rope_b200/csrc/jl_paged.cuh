@@ -294,6 +294,7 @@ struct PagedAppendArgs {
   long long table_stride;
   const int32_t *cu, *seqlens;
   int max_pages, page_log2, n_pages, T, max_new, Hkv, GS;
+  int heads;  // kv heads of a CTA
   long long page_stride;
 };
 cudaError_t launch_paged_append(bool bf16, int D, bool rotate, const PagedAppendArgs &a, const TurnFreq &turn,

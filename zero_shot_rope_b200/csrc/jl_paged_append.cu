@@ -13,7 +13,6 @@ namespace jl {
 
 namespace pga {
 
-constexpr int NT = 256;
 constexpr int CHUNK = 64;  // tokens whose angles are held at a time
 
 template <typename T>
@@ -50,7 +49,7 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// CTA (page of the sequence's new tokens, up to 8 kv heads, sequence): a page's
+// CTA (page of the sequence's new tokens, a.heads kv heads, sequence): a page's
 // new tokens, so that its ranges are reduced by one CTA, without atomics, and
 // its angles are formed once for all heads.  Keys and values: a thread has 16
 // bytes of the first half of a row and the partner 16 bytes of the second, of
@@ -60,11 +59,11 @@ struct Vec<__nv_bfloat16> {
 // thread asks for its next UNROLL rows before it works on the last ones, and two
 // CTAs share an SM: 32K tokens of 16/8 heads in 106 us, 5.1 TB/s, where a plain
 // copy of as many bytes takes 89 us.
-constexpr int HEADS = 8;
+constexpr int MAX_HEADS = 8;
 constexpr int UNROLL = 2;
 
-template <typename T, int D, bool ROT>
-__global__ void __launch_bounds__(NT, 2)
+template <typename T, int D, bool ROT, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT)
 paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_constant__ TurnFreq turn) {
   constexpr int N = Vec<T>::N, HALF = D / 2, CT = HALF / N;
   // the angles of CHUNK tokens (two neighbouring pairs: cos, cos, sin, sin), then the threads' ranges
@@ -72,7 +71,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
   __shared__ __align__(16) uint8_t smem[ANG > RED ? ANG : RED];
   float4(*cs)[HALF / 2] = reinterpret_cast<float4(*)[HALF / 2]>(smem);
   float(*red)[NT] = reinterpret_cast<float(*)[NT]>(smem);
-  const int b = blockIdx.z, h0 = blockIdx.y * HEADS, heads = min(HEADS, a.Hkv - h0);
+  const int b = blockIdx.z, h0 = blockIdx.y * a.heads, heads = min(a.heads, a.Hkv - h0);
   // (a thread's angles are all of one frequency, read once: lanes that read
   // different constants take turns)
   static_assert(NT % HALF == 0, "one frequency per thread");
@@ -237,11 +236,26 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
 }
 
 template <typename T, int D>
-cudaError_t launch(bool rotate, const PagedAppendArgs &a, const TurnFreq &turn, int batch, cudaStream_t st) {
+cudaError_t launch(bool rotate, const PagedAppendArgs &args, const TurnFreq &turn, int batch, cudaStream_t st) {
+  PagedAppendArgs a = args;
   const int P = 1 << a.page_log2;
-  const dim3 grid((unsigned)(((long long)a.max_new + 2 * P - 2) / P), (a.Hkv + HEADS - 1) / HEADS, batch);
-  const auto kernel = rotate ? paged_append_kernel<T, D, true> : paged_append_kernel<T, D, false>;
-  return launch_overlapped(kernel, grid, NT, 0, st, a, turn);
+  const long long slots = ((long long)a.max_new + 2 * P - 2) / P;
+  // all heads of a page in one CTA, up to 8, unless there are too few CTAs to fill
+  // the GPU (22 sequences of 181 tokens, 12/4 heads, 128-key pages: 20 us against
+  // 43; one token of one sequence: 3.7 against 5.1)
+  a.heads = a.Hkv < MAX_HEADS ? a.Hkv : MAX_HEADS;
+  while (a.heads > 1 && slots * batch * ((a.Hkv + a.heads - 1) / a.heads) < 2 * 148) a.heads = (a.heads + 1) / 2;
+  const dim3 grid((unsigned)slots, (a.Hkv + a.heads - 1) / a.heads, batch);
+  // a page of few rows keeps few threads busy, and more CTAs fit (32K tokens of 2/1
+  // heads in 16-key pages, fp32, 768 pieces: 30 us against 39; 64 x 150 tokens of
+  // 8/2 heads, 1280 pieces: 12 us against 9, so those keep 256 threads)
+  const long long pieces = (long long)(P < a.max_new ? P : a.max_new) * a.heads * (1 + a.GS) * D * sizeof(T) / 32;
+  if (pieces <= 1024) {
+    const auto kernel = rotate ? paged_append_kernel<T, D, true, 128> : paged_append_kernel<T, D, false, 128>;
+    return launch_overlapped(kernel, grid, 128, 0, st, a, turn);
+  }
+  const auto kernel = rotate ? paged_append_kernel<T, D, true, 256> : paged_append_kernel<T, D, false, 256>;
+  return launch_overlapped(kernel, grid, 256, 0, st, a, turn);
 }
 
 }  // namespace pga

@@ -686,7 +686,8 @@ cudaError_t launch(const PagedSelectArgs &args, const InvFreq &inv, const TurnFr
   const dim3 grid(a.Hkv, a.B);
   if (a.max_pages <= 512) return launch_overlapped(select_kernel<T, D, 128, 4>, grid, 128, 0, st, a, inv);
   if (a.max_pages <= 2048) return launch_overlapped(select_kernel<T, D, 512, 4>, grid, 512, 0, st, a, inv);
-  return launch_overlapped(select_kernel<T, D, 512, 16>, grid, 512, 0, st, a, inv);
+  if (a.max_pages <= 4096) return launch_overlapped(select_kernel<T, D, 1024, 4>, grid, 1024, 0, st, a, inv);
+  return launch_overlapped(select_kernel<T, D, 1024, 8>, grid, 1024, 0, st, a, inv);
 }
 
 }  // namespace pgs
