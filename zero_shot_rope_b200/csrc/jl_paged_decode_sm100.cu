@@ -72,7 +72,7 @@ __device__ __forceinline__ void tma_load5(const CUtensorMap *map, uint64_t *bar,
 }
 // Bounded waits whose probe may suspend the warp for up to SUSPEND_NS (a hint)
 // before it gives the answer: warps that poll take issue slots from those that
-// turn keys (16 x 32K tokens: 398 us with the default, 385 us so).
+// turn keys (64 sequences of 1K to 2K: 90 us with the default, 87 us so).
 constexpr uint32_t SUSPEND_NS = 2000;
 __device__ __forceinline__ bool mbar_try_long(uint64_t *b, uint32_t parity) {
   uint32_t ok;
