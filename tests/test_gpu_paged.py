@@ -304,6 +304,32 @@ def test_append_keeps_a_nan_in_the_summary():
         assert nan[1, 1, :, 5].all() and nan.sum() == 2
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_append_at_the_last_positions(dtype):
+    # lengths up to 2^31 - 1: no table reaches there, so nothing is written but
+    # the rotated queries; the first row of a page, whole pages and a part of one
+    J = jl()
+    lens, new, D, theta = (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 65), (1, 127, 300, 70), 64, 1e4
+    T = sum(new)
+    g = torch.Generator().manual_seed(31)
+    q, k = torch.randn(T, 4, D, generator=g).to(dtype), torch.randn(T, 2, D, generator=g).to(dtype)
+    half = 2.0 ** -8 if dtype == BF else P.U
+    for page in (16, 256):
+        kp = torch.full((3, page, 2, D), 3.0, dtype=dtype, device=DEV)
+        vp, sm = kp.clone(), torch.full((3, 2, 2, D), 3.0, dtype=dtype, device=DEV)
+        cu = np.concatenate([[0], np.cumsum(new)])
+        qo = J.jl_paged_append(k.to(DEV), k.to(DEV), kp, vp, i32([[0, 1, 2]] * 4), i32(cu), i32(lens), max(new),
+                               page_summary=sm, q=q.to(DEV), rope_theta=theta)
+        torch.cuda.synchronize()
+        assert all(bool((x == 3.0).all()) for x in (kp, vp, sm))
+        for b, (L, n) in enumerate(zip(lens, new)):
+            rows = slice(cu[b], cu[b + 1])
+            want = P.rotate(P.f64(q[rows]), np.arange(L - n, L)[:, None], theta)
+            # cosine, sine, a product and a sum in fp32; the angle's frequency and product in 64 bits, on either side
+            tol = half * np.abs(want) + (6 * P.U + 6 * 2.0 ** 31 * 2.0 ** -53) * P.pair_len(P.f64(q[rows]))
+            P.check(qo[rows].cpu(), want, tol, f"sequence {b}")
+
+
 # ------------------------------------------------------------------ select
 SELECT = [
     # lens, page, Hq, Hkv, D, dtype, w_pre, w0, n_select, n_first, n_last

@@ -109,8 +109,8 @@ paged_append_kernel(const __grid_constant__ PagedAppendArgs a, const __grid_cons
     }
   };
 
-  for (int j0 = ja; j0 < je; j0 += CHUNK) {
-    const int m = min(CHUNK, je - j0);
+  for (int done = 0; done < je - ja; done += CHUNK) {  // (counted from ja: positions go up to 2^31 - 2)
+    const int j0 = ja + done, m = min(CHUNK, je - j0);
     const size_t tok0 = (size_t)c0 + (size_t)(j0 - (L - n));
     if constexpr (ROT) {
       __syncthreads();
