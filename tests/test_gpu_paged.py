@@ -144,6 +144,46 @@ def test_decode_shows_a_nan_key_and_no_other(dtype):
     P.check(out[0, :2], ro[0, :2], to[0, :2], "other kv head")
 
 
+INF = float("inf")
+
+
+def _turn(j, L, w_pre, w0):
+    G = P.group(L, w_pre)
+    return (j // G - j) - ((L - 1) // G - (L - 1)) if j < L - w0 else 0
+
+
+@pytest.mark.parametrize("dtype,D,page", [(BF, 128, 16), (BF, 128, 64), (BF, 64, 32), (F32, 64, 16)])
+@pytest.mark.parametrize("j", [7, 1000, 1180, 1299])  # turned, turned, in the block with keys of both kinds, local
+def test_decode_of_an_infinite_key(dtype, D, page, j):
+    # one channel of a key of kv head 1 is infinite.  Queries with the sign that
+    # makes its score -inf drop the key; one with the other sign has a score of
+    # +inf, so its softmax is NaN, as in 64 bits
+    L, w_pre, w0, theta, d = 1300, 300, 117, 1e4, 5
+    assert page >= 16 and 1180 // 16 == (L - w0) // 16 and 1180 < L - w0
+    q = torch.randn(2, 8, D, generator=torch.Generator().manual_seed(j)).to(dtype)
+    kp, vp, table, keys, vals = P.make_cache((L, 400), page, 2, D, dtype, 6)
+    kp[table[0, j // page], j % page, 1, d] = INF
+    far = [k.clone() for k in keys]
+    far[0][j, 1, d] = 1e30  # for the 64-bit form: a score so low that the weight is zero there too
+    tame = [k.clone() for k in keys]
+    tame[0][j, 1, d] = 0.0  # for the tolerances, which are those of the other keys
+    turned = P.rotate(P.f64(far[0][j, 1]), _turn(j, L, w_pre, w0), theta)
+    for x in np.flatnonzero(np.abs(turned) > 1e20):  # the channel, and its partner if the key is turned
+        q[0, 4:, x] = q[0, 4:, x].abs() * -float(np.sign(turned[x]))
+    for plus in (False, True):
+        ro, rl, _, _ = P.decode(q, far, vals, w_pre, w0, theta)
+        _, _, to, tl = P.decode(q, tame, vals, w_pre, w0, theta)
+        if plus:
+            q[0, 6] = -q[0, 6]
+        out, lse = run_decode(q, kp.to(DEV), vp.to(DEV), table, (L, 400), w_pre, w0, theta)
+        if plus:
+            assert torch.isnan(out[0, 6]).all() and torch.isnan(lse[0, 6])
+        keep = [0, 1, 2, 3, 4, 5, 7] + ([] if plus else [6])
+        P.check(out[0, keep], ro[0, keep], to[0, keep], "out")
+        P.check(lse[0, keep], rl[0, keep], tl[0, keep], "lse")
+        P.check(out[1], ro[1], to[1], "the other sequence")
+
+
 def test_decode_large_scores_and_one_hot():
     # a single key dominates by far (scores beyond exp's range apart)
     lens, page = (2000,), 64

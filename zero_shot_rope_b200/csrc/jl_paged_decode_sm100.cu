@@ -419,14 +419,18 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
                 mma(c, bh[0], bh[1], bh[2], bh[3], qf[D / 32 + x][0], qf[D / 32 + x][1]);
                 mma(cl, bl[0], bl[1], bl[2], bl[3], qf[D / 32 + x][0], qf[D / 32 + x][1]);
               }
+              // where an element is infinite its high half alone says so: what is left of it
+              // is inf - inf, and a low half times an infinite query may be 0 inf
+#pragma unroll
+              for (int e = 0; e < 4; ++e) cl[e] = isnan(c[e] + cl[e]) ? c[e] : c[e] + cl[e];
               if (j0 + PD_BLK > j_local) {  // the one block with keys of both kinds
                 plain_scores();
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (j0 + row + 8 * (e >> 1) < j_local) sc[e] = c[e] + cl[e];
+                  if (j0 + row + 8 * (e >> 1) < j_local) sc[e] = cl[e];
               } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[e] = c[e] + cl[e];
+                for (int e = 0; e < 4; ++e) sc[e] = cl[e];
               }
             }
             // mask, in units of log2 e
