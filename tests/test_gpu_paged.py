@@ -184,6 +184,35 @@ def test_decode_of_an_infinite_key(dtype, D, page, j):
         P.check(out[1], ro[1], to[1], "the other sequence")
 
 
+@pytest.mark.parametrize("dtype,D,page", [(BF, 128, 16), (BF, 128, 64), (BF, 64, 32), (F32, 64, 16)])
+def test_decode_of_infinite_and_nan_values(dtype, D, page):
+    # an infinite value makes its channel infinite for its own heads, two of
+    # opposite signs or a NaN make it NaN; a key's weight may have any bits: all
+    # keys are tried in turn, one channel each, turned and local ones
+    L, w_pre, w0, theta = 900, 200, 333, 1e4
+    q = torch.randn(1, 8, D, generator=torch.Generator().manual_seed(D)).to(dtype)
+    kp, vp, table, keys, vals = P.make_cache((L,), page, 2, D, dtype, 16)
+    tol = P.decode(q, keys, vals, w_pre, w0, theta)[2]
+    kd = kp.to(DEV)
+    for first in range(0, L, 3 * D // 4):
+        v2, want = vp.clone(), vals[0].clone()
+        for x in range(min(3 * D // 4, L - first)):
+            j, what = first + x, (INF, -INF, float("nan"))[x % 3]
+            want[j, x % 2, x] = what
+            v2[table[0, j // page], j % page, x % 2, x] = what
+        want[(first + 200) % L, 0, 0] = -INF  # beside the +inf of channel 0
+        v2[table[0, (first + 200) % L // page], (first + 200) % L % page, 0, 0] = -INF
+        with np.errstate(invalid="ignore"):
+            ro = P.decode(q, keys, [want], w_pre, w0, theta)[0]
+        out, lse = run_decode(q, kd, v2.to(DEV), table, (L,), w_pre, w0, theta)
+        got = to_np(out)
+        assert np.array_equal(np.isnan(got), np.isnan(ro)), first
+        assert np.isnan(ro[0, :4, 0]).all() and (np.abs(ro[0]) == INF).any()
+        there = ~np.isnan(ro)
+        P.check(np.where(there, got, 0.0), np.where(there, ro, 0.0), tol, f"from key {first}")
+        assert torch.isfinite(lse).all()
+
+
 def test_decode_large_scores_and_one_hot():
     # a single key dominates by far (scores beyond exp's range apart)
     lens, page = (2000,), 64

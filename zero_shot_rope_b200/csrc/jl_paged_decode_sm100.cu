@@ -23,8 +23,10 @@
 // and that of step x + D/32), so the rotation happens on the operand's own
 // registers.  At the memory's pace a tile leaves an SM some 1400 cycles.
 //
-// Precision: turned keys and softmax weights are split into two bf16, hi + lo,
-// and both are multiplied, so neither is rounded to eight bits; scores, maxima,
+// Precision: turned keys are split into two bf16, hi + lo, and both are
+// multiplied, so they are held to 2^-17; softmax weights are split into three,
+// which hold all their bits (three for the keys as well would be 16 further
+// products and 128 further instructions per 16 keys and warp); scores, maxima,
 // sums and outputs are fp32.
 #include "jl_paged.cuh"
 #include "jl_ptx.cuh"
@@ -165,6 +167,23 @@ __device__ __forceinline__ uint64_t pack2(float x, float y) {
 __device__ __forceinline__ void split2(uint64_t x, uint32_t &hi, uint32_t &lo) {
   hi = f2_bf2(x);
   lo = f2_bf2(sub2(x, bf2_f2(hi)));
+}
+// Two weights x, y >= 0 as three bf16 pairs, whose sums they are: 3 x 8 bits by
+// truncation.  No part is negative, and none is 0 where the weight is not (at
+// least 2^-24 of it): each part's product with an infinite value then is that
+// infinity, not 0 inf or an infinity of the other sign.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    p[i] = __byte_perm(a, b, 0x7632);
+    x -= __uint_as_float(a & 0xffff0000u);
+    y -= __uint_as_float(b & 0xffff0000u);
+  }
+  uint32_t least;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(least) : "r"(p[0]), "r"(0x33803380u));  // 2^-24
+  asm("max.bf16x2 %0, %0, %1;" : "+r"(p[1]) : "r"(least));
+  asm("max.bf16x2 %0, %0, %1;" : "+r"(p[2]) : "r"(least));
 }
 
 template <int D>
@@ -462,16 +481,16 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
 #pragma unroll
               for (int x = 0; x < D / 16; ++x) o[x][0] *= f[0], o[x][1] *= f[1], o[x][2] *= f[0], o[x][3] *= f[1];
             }
-            // weights, high and low halves, turned into the second operand of the products with the values
+            // weights, in three parts, turned into the second operand of the products with the values
             const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
-            uint32_t ph[2], pl[2];
+            uint32_t pw[2][3];
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb) {
               const float e0 = ex2(sc[2 * nb] - m0), e1 = ex2(sc[2 * nb + 1] - m1);
               l[0] += e0, l[1] += e1;
-              split2(pack2(e0, e1), ph[nb], pl[nb]);
-              ph[nb] = transpose8(ph[nb]);
-              pl[nb] = transpose8(pl[nb]);
+              split3(e0, e1, pw[nb]);
+#pragma unroll
+              for (int i = 0; i < 3; ++i) pw[nb][i] = transpose8(pw[nb][i]);
             }
             uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of keys 2 q4 + {0, 1} (+ 8)
             if (part) {
@@ -491,8 +510,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
                 vf[0] &= keep[0], vf[1] &= keep[0];
                 vf[2] &= keep[1], vf[3] &= keep[1];
               }
-              mma(o[x], vf[0], vf[1], vf[2], vf[3], ph[0], ph[1]);
-              mma(o[x], vf[0], vf[1], vf[2], vf[3], pl[0], pl[1]);
+#pragma unroll
+              for (int i = 0; i < 3; ++i) mma(o[x], vf[0], vf[1], vf[2], vf[3], pw[0][i], pw[1][i]);
             }
           }
           __syncwarp();
