@@ -1,4 +1,6 @@
 """The paged-cache operators on the GPU against plain 64-bit forms."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -646,6 +648,36 @@ def test_decode_returns_whatever_the_wait_limit(D):
         P.check(first, ro, to, "out under the short limit")
     P.check(out, ro, to, "out")
     P.check(lse, rl, tl, "lse")
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (128, 16), (64, 64)])
+def test_decode_reports_a_wait_that_ran_out(D, page):
+    # With the limit at 1 ns the first wait for a tile, whose load takes a
+    # thousand times that, gives up: every role stops, the loads in flight are
+    # let land (which takes no further time-out), the error word says so, and
+    # the next call is right.
+    J = jl()
+    lens = (30000, 9000)
+    q = torch.randn(2, 8, D, generator=torch.Generator().manual_seed(1)).to(BF)
+    kp, vp, table, keys, vals = P.make_cache(lens, page, 2, D, BF, 5)
+    kd, vd, qd, td, ld = kp.to(DEV), vp.to(DEV), q.to(DEV), i32(table), i32(lens)
+    want, _ = run_decode(q, kd, vd, table, lens, 8000, 100, 1e4)
+    ws = torch.zeros(J.jl_bifocal_decode_paged_workspace_size(2, D), dtype=torch.uint8, device=DEV)
+    for _ in range(5):
+        try:
+            assert J.lib().jl_debug_set_wait_limit(1) == 0
+            began = time.perf_counter()
+            J.jl_bifocal_decode_paged(qd, kd, vd, td, ld, 8000, 100, 1e4, workspace=ws)
+            torch.cuda.synchronize()
+            took = time.perf_counter() - began
+        finally:
+            assert J.lib().jl_debug_set_wait_limit(0) == 0
+        assert int(ws[:4].view(torch.int32)) == 64
+        assert took < 1.0  # a time-out while the loads land would be 2 s
+        out, _ = run_decode(q, kd, vd, table, lens, 8000, 100, 1e4)
+        assert torch.equal(out, want)
+    ro, _, to, _ = P.decode(q, keys, vals, 8000, 100, 1e4)
+    P.check(out, ro, to, "out")
 
 
 @pytest.mark.parametrize("D,page", [(128, 64), (64, 16)])

@@ -72,6 +72,12 @@ __device__ __forceinline__ void tma_load5(const CUtensorMap *map, uint64_t *bar,
       "l"(map), "r"(su32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
+// What the roles' bounded waits share, in shared memory.
+struct Waits {
+  volatile int abort;
+  int err;
+  unsigned long long limit;  // ns
+};
 // Bounded waits whose probe may suspend the warp for up to SUSPEND_NS (a hint)
 // before it gives the answer: warps that poll take issue slots from those that
 // turn keys (64 sequences of 1K to 2K: 90 us with the default, 87 us so).
@@ -87,22 +93,23 @@ __device__ __forceinline__ bool mbar_try_long(uint64_t *b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-static __device__ __noinline__ bool wait_long_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err) {
+template <bool LONG>
+static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, Waits *w) {
   const uint64_t t0 = gtime();
-  const uint64_t limit = *(volatile unsigned long long *)&g_wait_limit_ns;
+  const uint64_t limit = w->limit;
   for (;;) {
-    if (mbar_try_long(bar, parity)) return true;
-    if (*abort_flag) return false;
+    if (LONG ? mbar_try_long(bar, parity) : mbar_test(bar, parity)) return true;
+    if (w->abort) return false;
     if (gtime() - t0 > limit) {
-      *abort_flag = 1;
-      atomicOr(err, ERR_TIMEOUT);
+      w->abort = 1;
+      atomicOr(&w->err, ERR_TIMEOUT);
       return false;
     }
   }
 }
-__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err) {
+__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, Waits *w) {
   if (mbar_try_long(bar, parity)) return true;
-  return wait_long_slow(bar, parity, abort_flag, err);
+  return wait_slow<true>(bar, parity, w);
 }
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -196,8 +203,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
   __shared__ __align__(8) uint64_t bar_full[NST], bar_empty[NST];
   __shared__ int s_j0[NST][NBLK], s_rho[NST][NBLK];  // a block's first key, and its remainder by G
   __shared__ float red_ml[NCW][PD_HEADS][2];
-  __shared__ volatile int abort_flag;
-  __shared__ int err_s, issued;  // tiles whose loads were issued
+  __shared__ Waits waits;
+  __shared__ int issued, announced[2];  // tiles whose loads were issued; the first tile of each group whose angles were not announced
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = (su32(smem_raw) + 1023u) & ~1023u;
   uint8_t *gbase = smem_raw + (sbase - su32(smem_raw));
@@ -207,8 +214,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       mbar_init(&bar_full[s], 2);       // producer, angles
       mbar_init(&bar_empty[s], NBLK);   // the four consumer warps of the tile
     }
-    abort_flag = 0;
-    err_s = issued = 0;
+    waits.abort = waits.err = 0;
+    issued = announced[0] = announced[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // turns by r = 0 .. 15 positions: {cos, cos, sin, sin} of two neighbouring
@@ -226,6 +233,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
   }
   let_next_kernel_come();
   wait_for_kernel_before();
+  if (threadIdx.x == 0) waits.limit = *(volatile unsigned long long *)&g_wait_limit_ns;
   const PagedRun run = paged_plan<THREADS>(p);
   __syncthreads();
 
@@ -253,7 +261,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           const unsigned boxes = __ballot_sync(0xffffffffu, leads && want != 0);
           for (int x = 0; x < 8 && u + x < w.u1; ++x, ++it) {
             const int st = it % NST;
-            if (it >= NST) ok = wait_long(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s);
+            if (it >= NST) ok = wait_long(&bar_empty[st], ((it / NST) - 1) & 1, &waits);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const bool mine = (lane >> 2) == x;
@@ -307,7 +315,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
                 for (int e = 0; e < HALF / 32; ++e) turn_cs(nb, tw[e], c[blk][e], s[blk][e]);
               }
             }
-            if (it >= NST) ok = wait_long(&bar_empty[st], ((it / NST) - 1) & 1, &abort_flag, &err_s);
+            if (it >= NST) ok = wait_long(&bar_empty[st], ((it / NST) - 1) & 1, &waits);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (any) {
@@ -328,6 +336,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
           }
         }
       }
+      if (lane == 0) announced[par] = it;
     } else {
       // ======================= consumers =======================
       const int blk = warp & 3, par = warp >> 2;
@@ -344,6 +353,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
       const int k_ch = lm >> 1, v_ch = lm & 1;  // 8-channel chunk of a 16-channel step
       int it = 0;
       bool ok = true;
+      // the hardware suspends for longer than a limit below SUSPEND_NS, whatever the
+      // hint: such a one is kept by looks at the group's first tile that do not suspend
+      if (waits.limit < SUSPEND_NS && run.t1 - run.t0 > par) ok = wait_slow<false>(&bar_full[par], 0, &waits);
       while (w.next(p)) {
         const int kvh = w.pair / p.HB, hb = w.pair % p.HB;
         const int gh = min(PD_HEADS, p.GS - hb * PD_HEADS);
@@ -375,7 +387,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
         for (int u = w.u0; u < w.u1; ++u, ++it) {
           if ((it & 1) != par) continue;
           const int st = it % NST;
-          if (ok) ok = wait_long(&bar_full[st], (it / NST) & 1, &abort_flag, &err_s);
+          if (ok) ok = wait_long(&bar_full[st], (it / NST) & 1, &waits);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;  // the run is walked to its end, so that the merges' barriers are met
           const int j0 = s_j0[st][blk];
@@ -568,12 +580,14 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_cons
     }
   }
   __syncthreads();
-  // after a timeout, let the loads in flight land (some role may have left a
-  // stage's barrier incomplete: these waits end too)
-  if (threadIdx.x == 0 && abort_flag)
-    for (int x = max(0, issued - NST); x < issued; ++x)
-      wait_drain(&bar_full[x % NST], (x / NST) & 1, &err_s, ERR_TIMEOUT);
-  if (threadIdx.x == 0) p.cta_err[blockIdx.x] = err_s;
+  // after a timeout, let the loads in flight land; a stage whose angles were not
+  // announced is announced here, so that its barrier waits for the loads alone
+  if (threadIdx.x == 0 && waits.abort)
+    for (int x = max(0, issued - NST); x < issued; ++x) {
+      if (x >= announced[x & 1]) mbar_arrive(&bar_full[x % NST]);
+      wait_drain(&bar_full[x % NST], (x / NST) & 1, &waits.err, ERR_TIMEOUT);
+    }
+  if (threadIdx.x == 0) p.cta_err[blockIdx.x] = waits.err;
 }
 
 static bool make_pool_map(CUtensorMap *m, const void *base, const PagedDecodeArgs &a, int D) {
