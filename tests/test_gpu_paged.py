@@ -463,6 +463,26 @@ def test_select_of_scores_that_fp32_cannot_tell_apart(kind, dtype):
         assert want[0, 0].tolist() == list(range(n - 1)) + [699]
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_select_with_a_base_below_one(dtype):
+    # frequencies 1, 2, 4 .. 2^31 (exact in 64 bits, and so are their angles), of
+    # which the queries use the highest: angles up to 2^44, whose fractions of a
+    # turn decide the scores
+    J = jl()
+    page, Hkv, D, L, n = 16, 32, 64, 8192, 256
+    g = torch.Generator().manual_seed(12)
+    q = torch.zeros(2, Hkv, D)
+    q[..., [31, 63]] = torch.randn(2, Hkv, 2, generator=g)
+    q = q.to(dtype)
+    table = torch.randperm(L // page, generator=g).to(torch.int32)[None].repeat(2, 1)
+    base = torch.randn(L // page, Hkv, 1, D, generator=g)
+    sm = torch.cat((base - 0.1, base + 0.1), 2).to(dtype)
+    lens = (L, L - 777)
+    got = J.jl_bifocal_select_pages(q.to(DEV), sm.to(DEV), i32(table), i32(lens), page, n, 64, 16, 2.0 ** -32)
+    want = P.select(q, sm, table, lens, page, n, 1, 1, 64, 16, 2.0 ** -32)
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_select_passes_over_pages_that_are_not_there():
     J = jl()
     g = torch.Generator().manual_seed(6)

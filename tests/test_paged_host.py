@@ -272,6 +272,34 @@ def test_turns_match_64_bit_angles():
     assert c.value == 1.0 and s.value == 0.0
 
 
+def test_turns_of_high_frequencies():
+    # bases below 1 have frequencies above 1: cos and sin within 3 steps of 2^-24
+    # of those of the exact product, at every position (worked out in whole numbers)
+    from decimal import Decimal, getcontext
+
+    getcontext().prec = 140
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534"
+                         "211706798214808651328230664709384460955058223172535940812848111745")
+    per_turn = int((1 / two_pi) * (1 << 400))  # 1 / (2 pi), in 2^-400
+    jl = _lib()
+    L = jl.lib()
+    L.jl_debug_turn_cs.argtypes = [ctypes.c_int32, ctypes.c_double, ctypes.POINTER(ctypes.c_float),
+                                   ctypes.POINTER(ctypes.c_float)]
+    c, s = ctypes.c_float(), ctypes.c_float()
+    rng = np.random.default_rng(2)
+    worst = 0.0
+    for theta in (1e6, 0.5, 1e-3, 1e-12, 2.0 ** -32):
+        for k in range(0, 64, 3):
+            w = theta ** (-2.0 * k / 128)
+            num, den = w.as_integer_ratio()
+            for n in [1, -3, 2 ** 30, -(2 ** 30) + 1, 2 ** 31 - 1] + rng.integers(-2 ** 30, 2 ** 30, 25).tolist():
+                turns = (n * num * per_turn // den) & ((1 << 400) - 1)
+                a = float(Decimal(turns) / (1 << 400) * two_pi)
+                L.jl_debug_turn_cs(int(n), w, ctypes.byref(c), ctypes.byref(s))
+                worst = max(worst, abs(c.value - np.cos(a)), abs(s.value - np.sin(a)))
+    assert worst <= 3 * 2.0 ** -24, worst * 2.0 ** 24
+
+
 def test_packed_call_checks_its_words():
     import struct
 

@@ -62,12 +62,22 @@ jl::InvFreq make_inv_freq(int D, double theta) {
   return f;
 }
 
-// The same frequencies in turns per position, times 2^64 (modulo a turn).
+// x modulo 1, times 2^64, to 2^-64 of a turn.
+unsigned long long turn_bits(double x) {
+  const double r = x - std::rint(x);  // exact
+  return std::isfinite(r) ? (unsigned long long)std::llrint(std::ldexp(r, 63)) << 1 : 0ull;
+}
+
+// The same frequencies in turns per position, times 2^64 (modulo a turn).  1/(2 pi)
+// as the sum of three doubles, so that a frequency above 1 keeps its fraction of
+// a turn: the angle of any 31-bit number of positions is then known to 2^-30 turns.
 jl::TurnFreq make_turn_freq(const jl::InvFreq &inv) {
+  constexpr double c1 = 0x1.45f306dc9c883p-3, c2 = -0x1.6b01ec5417056p-57, c3 = -0x1.6447e493ad4cep-111;
   jl::TurnFreq f;
   for (int k = 0; k < JL_MAX_HALF; ++k) {
-    const double t = inv.v[k] * 0.15915494309189533577;  // 1 / (2 pi)
-    f.v[k] = (unsigned long long)std::ldexp(t - std::floor(t), 64);
+    const double w = inv.v[k], p1 = w * c1, p2 = w * c2;
+    f.v[k] = turn_bits(p1) + turn_bits(std::fma(w, c1, -p1)) + turn_bits(p2) + turn_bits(std::fma(w, c2, -p2)) +
+             turn_bits(w * c3);
   }
   return f;
 }

@@ -482,7 +482,10 @@ __device__ uint32_t kth_largest_held(const uint32_t (&key)[R], int k) {
 // most 7u (cosine and sine within 3u, one product, one sum), hi + lo and
 // hi - lo by 1u each, and a term goes through at most 8 + 5 further sums:
 // 22u = 1.32e-6.  1.9e-6 is used (and twice that for twice the score), as the norms and thresholds are rounded too;
-// 2e-18 makes up for squares and 1e-36 for products below the normal range.
+// 2e-18 makes up for squares and 1e-36 for products below the normal range.  The
+// angles in 64 bits are themselves products rounded to 2^-53, which moves the turned
+// query by at most L 2^-53 times the highest frequency (far below 1.9e-6 unless
+// positions are near 2^30 or the base is below 1).
 template <typename T, int D, int NT_SEL, int R>
 __global__ void __launch_bounds__(NT_SEL)
 select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__ InvFreq inv) {
@@ -545,7 +548,8 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
     float m2 = 0.f, q2 = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) m2 = max_nan(m2, s_max[0][w]), q2 = max_nan(q2, s_max[1][w]);
-    const float eps = 3.8e-6f * (sqrtf(q2) + 2e-18f) * (sqrtf(m2) + 2e-18f) + 1e-36f;
+    const float rel = 3.8e-6f + 2.4e-16f * (float)p.seqlens[b] * (float)fmax(inv.v[0], inv.v[D / 2 - 1]);
+    const float eps = rel * (sqrtf(q2) + 2e-18f) * (sqrtf(m2) + 2e-18f) + 1e-36f;
     if (eps < 1e30f) {  // no square or score near overflow, nothing infinite or NaN
       above_t = t + 2.f * eps;
       below_t = t - 2.f * eps;
