@@ -483,6 +483,50 @@ def test_select_with_a_base_below_one(dtype):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("n_near", [2, 3, 17, 64, 65, 130])
+@pytest.mark.parametrize("kind,dtype,Hq,D", [("local", BF, 2, 64), ("local", F32, 8, 128), ("slow", BF, 8, 128),
+                                             ("slow", F32, 2, 64), ("turned", F32, 8, 128), ("turned", F32, 2, 64)])
+def test_select_among_a_few_near_ties(kind, dtype, Hq, D, n_near):
+    # n_near pages whose scores differ by less than fp32 can show, in an order
+    # that is not that of the pages, half of them chosen; all others far above or
+    # below.  "local": no turn, differences in one channel, some exactly equal;
+    # "slow": turned, by frequencies that hardly matter; "turned": each page's
+    # keys turned so that the query meets the same ones, and rounded
+    J = jl()
+    page, Hkv, pages, n_high = 16, 2, 300, 9
+    L, w0, half = page * pages - 5, 40, D // 2
+    w_pre = 10 ** 6 if kind == "local" else 1000
+    theta = 1e12 if kind == "slow" else 1e4
+    g = torch.Generator().manual_seed(n_near + D)
+    q = torch.randn(1, Hq, D, generator=g).to(dtype)
+    first = q[0, ::Hq // Hkv].double()  # the query head that all keys favour
+    base = 100 * (1 + torch.rand(Hkv, D, generator=g).double()) * first.sign()
+    if kind == "slow":
+        base[:, :half - 4], base[:, half:D - 4] = 0.0, 0.0
+    order = torch.randperm(pages - 50, generator=g) + 10  # (the last pages are local: no near ties there)
+    near, high = order[:n_near], order[n_near:n_near + n_high]
+    size = torch.full((pages,), 0.3, dtype=torch.float64) - 0.2 * torch.rand(pages, generator=g).double()
+    size[near], size[high] = 1.0, 1.5
+    m = size[:, None, None] * base
+    fine = torch.randint(0, max(2, n_near // 2), (pages, Hkv), generator=g)
+    if kind == "turned":
+        G = P.group(L, w_pre)
+        mid = np.arange(pages) * page + page // 2
+        turn = np.where(mid < L - w0, (mid - mid // G) - ((L - 1) - (L - 1) // G), 0)
+        m = torch.from_numpy(P.rotate(m.numpy(), np.broadcast_to(turn[:, None], (pages, Hkv)), theta))
+    else:
+        m[near, :, D - 1] = 1e-5 * (1 + fine[near].double())
+    sm = torch.zeros(pages, Hkv, 2, D, dtype=dtype)
+    table = torch.randperm(pages, generator=g).to(torch.int32)[None]
+    sm[table[0].long()] = m[:, :, None].to(dtype).expand(-1, -1, 2, -1)
+    n = 2 + n_high + (n_near + 1) // 2
+    want = P.select(q, sm, table, [L], page, n, 1, 1, w_pre, w0, theta)
+    for h in range(Hkv):  # the case is what it says
+        assert set(high.tolist()) <= set(want[0, h]) <= set(high.tolist() + near.tolist() + [0, pages - 1])
+    got = J.jl_bifocal_select_pages(q.to(DEV), sm.to(DEV), i32(table), i32([L]), page, n, w_pre, w0, theta)
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_select_passes_over_pages_that_are_not_there():
     J = jl()
     g = torch.Generator().manual_seed(6)
@@ -723,6 +767,33 @@ def test_decode_at_full_pace_repeats(D, page):
     for _ in range(200):
         again, _ = J.jl_bifocal_decode_paged(q, kp, vp, table, ld, 1 << 20, 64, 1e4)
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (128, 16), (64, 16)])
+def test_every_decode_at_full_pace_is_the_same(D, page):
+    # as the test above, but every call's outputs and error word are looked at
+    # (on the GPU, so that the calls stay back to back)
+    J = jl()
+    lens = (65536, 31000)
+    g = torch.Generator(device=DEV).manual_seed(10)
+    n = [-(-x // page) for x in lens]
+    kp = torch.randn(sum(n), page, 2, D, generator=g, device=DEV).to(BF)
+    vp = torch.randn(sum(n), page, 2, D, generator=g, device=DEV).to(BF)
+    order = torch.randperm(sum(n), generator=g, device=DEV).to(torch.int32)
+    table = torch.zeros(2, max(n), dtype=torch.int32, device=DEV)
+    table[0, :n[0]], table[1, :n[1]] = order[:n[0]], order[n[0]:]
+    q = torch.randn(2, 8, D, generator=g, device=DEV).to(BF)
+    want = run_decode(q, kp, vp, table, lens, 1 << 20, 64, 1e4)
+    ld = i32(lens)
+    calls = 300
+    outs = torch.full((calls, 2, 8, D), float("nan"), dtype=BF, device=DEV)
+    lses = torch.full((calls, 2, 8), float("nan"), device=DEV)
+    ws = torch.full((calls, J.jl_bifocal_decode_paged_workspace_size(2, D)), 0xA5, dtype=torch.uint8, device=DEV)
+    for x in range(calls):
+        J.jl_bifocal_decode_paged(q, kp, vp, table, ld, 1 << 20, 64, 1e4, out=outs[x], lse=lses[x], workspace=ws[x])
+    torch.cuda.synchronize()
+    assert torch.equal(ws[:, :4].contiguous().view(torch.int32), torch.zeros(calls, 1, dtype=torch.int32, device=DEV))
+    assert torch.equal(outs, want[0].expand_as(outs)) and torch.equal(lses, want[1].expand_as(lses))
 
 
 @pytest.mark.parametrize("dtype,page", [(BF, 64), (F32, 32)])
