@@ -463,6 +463,18 @@ def test_select_of_scores_that_fp32_cannot_tell_apart(kind, dtype):
         assert want[0, 0].tolist() == list(range(n - 1)) + [699]
 
 
+def test_select_fills_the_longest_list():
+    # 2^31 - 1 entries, of which a short sequence has five
+    J = jl()
+    n = 2 ** 31 - 1
+    q, sm = torch.ones(1, 1, 64, device=DEV), torch.zeros(5, 1, 2, 64, device=DEV)
+    out = torch.full((1, 1, n), 77, dtype=torch.int32, device=DEV)
+    J.jl_bifocal_select_pages(q, sm, i32([[0, 1, 2, 3, 4]]), i32([70]), 16, n, 100, 10, 1e4, out=out)
+    assert out[0, 0, :5].tolist() == [0, 1, 2, 3, 4]
+    for a in range(5, n, 1 << 28):
+        assert bool((out[0, 0, a:a + (1 << 28)] == -1).all()), a
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_select_with_a_base_below_one(dtype):
     # frequencies 1, 2, 4 .. 2^31 (exact in 64 bits, and so are their angles), of

@@ -502,7 +502,7 @@ select_kernel(const __grid_constant__ PagedSelectArgs p, const __grid_constant__
   const size_t row = (size_t)b * p.Hkv + h;
   int32_t *list = p.list + row * p.n_select;
   if (pages <= p.n_select) {
-    for (int x = tid; x < p.n_select; x += NT_SEL) list[x] = x < pages ? x : -1;
+    for (unsigned x = tid; x < (unsigned)p.n_select; x += NT_SEL) list[x] = x < (unsigned)pages ? (int)x : -1;
     return;
   }
   float *score = p.score + row * p.max_pages;
