@@ -316,8 +316,9 @@ jl_status jl_bifocal_decode_noalloc_error(int32_t *error_word, void *stream);
  *                [0, n_pages) is a page that is not there.  Sequences may
  *                share pages that nobody writes.
  *   seqlens      [batch] device int32, L_b with the new tokens included.
- * max_pages * P <= 2^30.  Head counts: n_q_heads a multiple of n_kv_heads,
- * any group size; head_dim 64 or 128; batch <= 65535; JL_BF16 or JL_FP32.
+ * max_pages * P <= 2^30.  Head counts: n_q_heads <= 65535 a multiple of
+ * n_kv_heads, any group size; head_dim 64 or 128; batch <= 65535; JL_BF16 or
+ * JL_FP32.
  * All tables and lengths live on the device and are read when the kernels
  * run, so a captured call replays with the values of the moment.
  */

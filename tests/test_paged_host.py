@@ -132,6 +132,14 @@ def test_decode_refuses(kw, status):
     assert jl.status_string(_decode_raw(jl, **kw)) == status, jl.last_error()
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(65536, 2), (1 << 20, 1 << 20), (1 << 30, 1)])
+def test_more_heads_than_a_call_takes(Hq, Hkv):
+    jl = _lib()
+    for call in (_append_raw, _select_raw, _decode_raw):
+        kw = {} if call is _select_raw else dict(ps=16 * Hkv * 128)
+        assert jl.status_string(call(jl, Hq=Hq, Hkv=Hkv, **kw)) == "JL_ERR_UNSUPPORTED" and "heads" in jl.last_error()
+
+
 def test_empty_calls_are_no_ops():
     jl = _lib()
     assert _append_raw(jl, B=0) == jl.JL_OK and _append_raw(jl, T=0, new=0) == jl.JL_OK

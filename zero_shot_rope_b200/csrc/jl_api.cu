@@ -124,8 +124,10 @@ jl_status cuda_fail(cudaError_t e, const char *what) {
 }
 
 // What the paged-cache calls check alike.
-jl_status check_pages(int32_t page_size, int32_t n_pages, int32_t max_pages, int64_t table_stride, int32_t batch,
-                      jl_dtype dtype) {
+jl_status check_pages(int32_t n_q_heads, int32_t page_size, int32_t n_pages, int32_t max_pages, int64_t table_stride,
+                      int32_t batch, jl_dtype dtype) {
+  if (n_q_heads > kMaxGridY)
+    return fail(JL_ERR_UNSUPPORTED, "n_q_heads %d exceeds %d per call", n_q_heads, kMaxGridY);
   if (dtype != JL_BF16 && dtype != JL_FP32) return fail(JL_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
   if (page_size < 1 || (page_size & (page_size - 1)) != 0)
     return fail(JL_ERR_INVALID_ARG, "page_size must be a power of two (got %d)", page_size);
@@ -354,9 +356,7 @@ jl_status jl_paged_append(const void *k, const void *v, void *k_pages, void *v_p
                           double rope_theta, jl_dtype dtype, uint32_t flags, void *stream) {
   jl_status s;
   if ((s = check_heads(n_q_heads, n_kv_heads, head_dim)) != JL_OK) return s;
-  if (n_kv_heads > kMaxGridY)
-    return fail(JL_ERR_UNSUPPORTED, "n_kv_heads %d exceeds %d per call", n_kv_heads, kMaxGridY);
-  if ((s = check_pages(page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
+  if ((s = check_pages(n_q_heads, page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
   if ((s = check_pool(page_size, page_stride, n_kv_heads, head_dim, dtype)) != JL_OK) return s;
   if (flags & ~(uint32_t)JL_FLAG_ROTATE) return fail(JL_ERR_INVALID_ARG, "unknown or unfitting flag bits 0x%x", flags);
   const bool rotate = (flags & JL_FLAG_ROTATE) != 0;
@@ -414,7 +414,7 @@ jl_status jl_bifocal_select_pages(const void *q, const void *page_summary, const
   jl_status s;
   if ((s = check_heads(n_q_heads, n_kv_heads, head_dim)) != JL_OK) return s;
   if ((s = check_method(w_pretrained, w0, rope_theta)) != JL_OK) return s;
-  if ((s = check_pages(page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
+  if ((s = check_pages(n_q_heads, page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
   if (flags & ~(uint32_t)JL_FLAG_PLAIN_CAUSAL) return fail(JL_ERR_INVALID_ARG, "unknown or unfitting flag bits 0x%x", flags);
   if (n_select < 1) return fail(JL_ERR_INVALID_ARG, "n_select must be >= 1 (got %d)", n_select);
   if (n_first < 0 || n_last < 0 || (int64_t)n_first + n_last > n_select)
@@ -476,10 +476,8 @@ jl_status jl_bifocal_decode_paged(const void *q, const void *k_pages, const void
   jl_status s;
   if (window < 0) return fail(JL_ERR_INVALID_ARG, "window must be >= 0 (0: no window), got %d", window);
   if ((s = check_heads(n_q_heads, n_kv_heads, head_dim)) != JL_OK) return s;
-  if (n_q_heads > kMaxGridY)
-    return fail(JL_ERR_UNSUPPORTED, "n_q_heads %d exceeds %d per call", n_q_heads, kMaxGridY);
   if ((s = check_method(w_pretrained, w0, rope_theta)) != JL_OK) return s;
-  if ((s = check_pages(page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
+  if ((s = check_pages(n_q_heads, page_size, n_pages, max_pages, table_stride, batch, dtype)) != JL_OK) return s;
   if ((s = check_pool(page_size, page_stride, n_kv_heads, head_dim, dtype)) != JL_OK) return s;
   if (flags & ~(uint32_t)JL_FLAG_PLAIN_CAUSAL) return fail(JL_ERR_INVALID_ARG, "unknown or unfitting flag bits 0x%x", flags);
   if (n_list < 0 || n_list > (1 << 20)) return fail(JL_ERR_INVALID_ARG, "n_list must be in [0, 2^20] (got %d)", n_list);
