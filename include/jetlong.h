@@ -335,7 +335,8 @@ jl_status jl_bifocal_decode_noalloc_error(int32_t *error_word, void *stream);
  *   q, q_out     [total_tokens, Hq, D], rotated like k (q_out may be q); both
  *                NULL if not wanted.  Only with JL_FLAG_ROTATE.
  *   cu_seqlens   [batch + 1] device int32 prefix sums
- *   max_new      >= every sequence's number of new tokens (sizes the grid)
+ *   max_new      at least every sequence's number of new tokens (it sizes the
+ *                grid), from 1 to total_tokens
  *   rope_theta   used with JL_FLAG_ROTATE: pair k turns by
  *                p theta^(-2k/D) at position p (angles in 64 bits, the
  *                products in fp32, rounded once).  Without the flag k is

@@ -406,6 +406,7 @@ def jl_paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seqlens, ma
 
     With ``rope_theta`` k (and q [T, Hq, D], if given) arrive before RoPE and
     are rotated by their positions; without it k is stored as given.
+    ``max_new``, from 1 to T, is at least every sequence's number of new tokens.
     ``page_summary`` [n_pages, Hkv, 2, D], if given, is kept up to date.
     Returns the rotated q (``q_out``; it may be q itself) or None."""
     index = k.get_device()
