@@ -215,6 +215,27 @@ def test_decode_of_infinite_and_nan_values(dtype, D, page):
         assert torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_of_infinite_values_under_small_weights(dtype):
+    # scores 60 to 86 below the others', weights down to 2^-124
+    D, L = 64, 64
+    low = torch.linspace(-7.5, -10.75, 27)
+    q = torch.zeros(1, 1, D)
+    q[..., 0] = 64.0  # score = 8 k_0
+    kp, vp, table, keys, vals = P.make_cache((L,), 16, 1, D, dtype, 23)
+    k = torch.zeros(L, 1, D)
+    k[2:2 + len(low), 0, 0] = low
+    v = vals[0].clone()
+    for x in range(len(low)):
+        v[2 + x, 0, 2 * x], v[2 + x, 0, 2 * x + 1] = INF, -INF
+    for c in range(L // 16):
+        kp[table[0, c]], vp[table[0, c]] = k[c * 16:c * 16 + 16].to(dtype), v[c * 16:c * 16 + 16]
+    out, lse = run_decode(q.to(dtype), kp.to(DEV), vp.to(DEV), table, (L,), 10 ** 6, 8, 1e4)
+    assert out[0, 0, :2 * len(low):2].tolist() == [INF] * len(low)
+    assert out[0, 0, 1:2 * len(low):2].tolist() == [-INF] * len(low)
+    assert torch.isfinite(out[0, 0, 2 * len(low):]).all() and torch.isfinite(lse).all()
+
+
 def test_decode_large_scores_and_one_hot():
     # a single key dominates by far (scores beyond exp's range apart)
     lens, page = (2000,), 64
