@@ -421,9 +421,11 @@ jl_status jl_bifocal_select_pages(const void *q, const void *page_summary,
  *              each.
  * A sequence with no visible key (L_b = 0, a length past max_pages P, no page
  * of the list there) gets zeros and LSE = -inf.  Keys of pages that are not
- * there are not visible.  Scores, softmax statistics and outputs are held in
- * fp32; in bf16, keys that the bifocal rule turns and the softmax weights are
- * carried as pairs of bf16, so neither is rounded to eight bits.  The work is
+ * there are not visible.  Scores, softmax statistics, weights and outputs are
+ * held in fp32; in bf16, keys that the bifocal rule turns are carried as pairs of
+ * bf16, 17 bits (the LSE of a single such key is off by some 2e-6, of 64 by 4e-7).
+ * A key whose score is -inf is dropped; infinite values give infinities.  More than
+ * 8 query heads per kv head read the kv head's keys once for every 8.  The work is
  * divided over the SMs on the device, from the lengths, in a fixed order:
  * equal inputs give equal bits.
  */
