@@ -393,8 +393,10 @@ jl_status jl_paged_append(const void *k, const void *v, void *k_pages, void *v_p
   a.Hkv = n_kv_heads;
   a.GS = n_q_heads / n_kv_heads;
   a.page_stride = page_stride;
+  static const jl::TurnFreq none = {};  // (the thread's frequencies are kept for the calls that turn)
   const cudaError_t e = jl::launch_paged_append(dtype == JL_BF16, head_dim, rotate, a,
-                                                freqs_of(head_dim, rotate ? rope_theta : 1.0).turn, batch, (cudaStream_t)stream);
+                                                rotate ? freqs_of(head_dim, rope_theta).turn : none, batch,
+                                                (cudaStream_t)stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "paged append launch");
 }
 
