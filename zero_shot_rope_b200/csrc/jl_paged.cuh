@@ -36,7 +36,7 @@ struct TurnFreq {
 // the quadrant, the rest an angle within an eighth of a turn, whose sine and
 // cosine are the Taylor series in fp32 (to r^9 and r^10: truncated at 2e-9 and
 // 2e-10).  Off by less than 3 2^-24 from those of the exact product of n and the
-// frequency, whatever its size; about 25 instructions, against some 60 of 64-bit
+// frequency, up to 2^64 radians a position; about 25 instructions, against some 60 of 64-bit
 // arithmetic in angle_cs.
 __host__ __device__ __forceinline__ void turn_cs(int32_t n, unsigned long long w, float &c, float &s) {
   const unsigned long long x = (unsigned long long)(long long)n * w;

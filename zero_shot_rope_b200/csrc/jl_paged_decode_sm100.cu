@@ -25,7 +25,7 @@
 //
 // Precision: turned keys are split into two bf16, hi + lo, and both are
 // multiplied, so they are held to 2^-17; softmax weights are split into three,
-// which hold all their bits (three for the keys as well: 124 us against 111 at
+// which hold all their bits (three for the keys as well: 124 us against 112 at
 // 128K); scores, maxima, sums and outputs are fp32.
 #include "jl_paged.cuh"
 #include "jl_ptx.cuh"
